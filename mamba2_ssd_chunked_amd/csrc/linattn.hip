@@ -1,53 +1,29 @@
-// Linear attention with a decay per head: the walk over prompts (forward and, with the
-// operands in other roles, backward).
-//
-//   M_t = l M_(t-1) + s c_t b_t^T,   out_t = f M_t a_t
-//
-// One workgroup per (sequence, head): thread d keeps row d of M in registers and goes
-// through the tokens one by one, their a and b rows passing through LDS.
-#include "mixer_internal.h"
+// Linear attention with a decay per head over prompts: launches of the walk (la_walk.h),
+// the composition of span states and the sum over heads that share keys and values.
+#include "la_walk.h"
 
 namespace ssd {
 
-template <typename T, int BD>
-__global__ void __launch_bounds__(128) k_la_tokens(LaWalk w) {
-    __shared__ float sa[BD], sb[BD];
-    const int s = blockIdx.x / w.H, h = blockIdx.x % w.H, d = threadIdx.x;
+// States entering the spans of a sequence from the states its spans add: in place, slot
+// j >= 1 receives the state after span j - 1.  One lane per four state elements of a
+// (sequence, head).
+__global__ void __launch_bounds__(256) k_la_spans(LaWalk w, LaPlan plan, int quads,
+                                                 f32x4* __restrict__ ws) {
+    const int per = quads / 256, h = (int)(blockIdx.x / per % w.H);
+    const int s = (int)(blockIdx.x / per / w.H), q = (int)(blockIdx.x % per) * 256 + threadIdx.x;
     const SeqRange r = seq_range(w, s);
-    const int len = (int)(r.hi - r.lo);
-    const float l = expf(w.log_decay[h]);
-    const int64_t st = ((int64_t)s * w.H + h) * BD * w.cd;
-    const int64_t rs = w.trans ? 1 : BD, ks = w.trans ? w.cd : 1;
-    float M[BD];
-#pragma unroll
-    for (int e = 0; e < BD; ++e) M[e] = w.init ? w.init[st + d * rs + e * ks] : 0.f;
-    for (int i = 0; i < len; ++i) {
-        const int64_t t = w.reverse ? r.hi - 1 - i : r.lo + i;
-        const T* a = (const T*)w.a + t * w.a_ts + (h / w.a_div) * BD;
-        const T* b = (const T*)w.b + t * w.b_ts + (h / w.b_div) * BD;
-        for (int e = d; e < BD; e += blockDim.x) {
-            sa[e] = (float)a[e];
-            sb[e] = (float)b[e];
-        }
-        __syncthreads();
-        const float c = w.state_scale * (float)((const T*)w.c)[t * w.c_ts + (h / w.c_div) * w.cd + d];
-        const float keep = w.reverse && i == 0 ? 1.f : l;
-        float o = 0.f;
-#pragma unroll
-        for (int e = 0; e < BD; ++e) {
-            M[e] = M[e] * keep + c * sb[e];
-            o += M[e] * sa[e];
-        }
-        o *= w.inter;
-        const int64_t at = t * w.out_ts + (int64_t)h * w.cd + d;
-        if (w.out_f32) ((float*)w.out)[at] = o;
-        else ((T*)w.out)[at] = (T)o;
-        __syncthreads();
-    }
-    if (w.fin) {
-        const float keep = w.reverse && len > 0 ? l : 1.f;
-#pragma unroll
-        for (int e = 0; e < BD; ++e) w.fin[st + d * rs + e * ks] = M[e] * keep;
+    const int64_t n = (r.hi - r.lo + plan.span - 1) / plan.span;
+    if (n < 2) return;
+    const float keep = (float)exp((double)plan.span * (double)w.log_decay[h]);
+    const int64_t step = (int64_t)w.H * quads;
+    f32x4* p = ws + (r.lo / plan.span + s) * step + (int64_t)h * quads + q;
+    f32x4 m = *p;
+    for (int64_t j = 1; j < n; ++j) {
+        p += step;
+        f32x4 add = {0.f, 0.f, 0.f, 0.f};
+        if (j + 1 < n) add = *p;
+        *p = m;
+        m = m * keep + add;
     }
 }
 
@@ -68,22 +44,55 @@ __global__ void __launch_bounds__(256) k_la_group_sum(LaWalk w, const float* __r
     }
 }
 
+// Spans: two workgroups for each of the 256 CUs where the tokens allow it, but none
+// shorter than 256 tokens (a span costs a state's round trip and a pass over b and c).
+constexpr int LA_BLOCKS = 512, LA_MIN_SPAN = 256;
+
+static LaPlan la_plan(const LaWalk& w) {
+    const int64_t per = (w.tokens * w.H + LA_BLOCKS - 1) / LA_BLOCKS;
+    LaPlan p;
+    p.span = (int)((per > LA_MIN_SPAN ? per + 63 : LA_MIN_SPAN) / 64 * 64);
+    p.slots = w.tokens / p.span + w.nseq;
+    p.split = (w.cu ? w.tokens : w.seqlen) > p.span;
+    return p;
+}
+
+size_t la_walk_ws(const LaWalk& w, int) {
+    const LaPlan p = la_plan(w);
+    return p.split ? (size_t)p.slots * w.H * w.bd * w.cd * 4 : 0;
+}
+
+template <typename T, int BD, int CD>
+static hipError_t walk_shape(const LaWalk& w, f32x4* ws, hipStream_t s) {
+    constexpr bool B16 = sizeof(T) == 2;
+    const LaPlan p = la_plan(w);
+    const dim3 grid((unsigned)(p.slots * w.H)), block(256);
+    if (p.split) {
+        SSD_TRY(launch(k_la_walk<T, BD, CD, false, B16 ? 3 : 1>, grid, block, s, w, p, ws));
+        constexpr int quads = BD * CD / 4;
+        SSD_TRY(launch(k_la_spans, dim3((unsigned)((int64_t)w.nseq * w.H * (quads / 256))),
+                       dim3(256), s, w, p, quads, ws));
+    }
+    if (B16 && !w.fin) return launch(k_la_walk<T, BD, CD, true, B16 ? 2 : 1>, grid, block, s, w, p, ws);
+    return launch(k_la_walk<T, BD, CD, true, B16 ? 3 : 1>, grid, block, s, w, p, ws);
+}
+
+template <typename T>
+static hipError_t walk_t(const LaWalk& w, void* ws, hipStream_t s) {
+    if (w.bd == 64 && w.cd == 64) return walk_shape<T, 64, 64>(w, (f32x4*)ws, s);
+    if (w.bd == 64 && w.cd == 128) return walk_shape<T, 64, 128>(w, (f32x4*)ws, s);
+    if (w.bd == 128 && w.cd == 64) return walk_shape<T, 128, 64>(w, (f32x4*)ws, s);
+    if (w.bd == 128 && w.cd == 128) return walk_shape<T, 128, 128>(w, (f32x4*)ws, s);
+    return hipErrorInvalidValue;
+}
+
 bool la_supported(int keydim, int valdim, int act) {
     return (keydim == 64 || keydim == 128) && (valdim == 64 || valdim == 128) &&
            (act == SSD_F32 || act == SSD_BF16);
 }
 
-size_t la_walk_ws(const LaWalk&, int) { return 0; }
-
-template <typename T>
-static hipError_t walk_t(const LaWalk& w, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)w.nseq * w.H)), block(w.cd);
-    if (w.bd == 64) return launch(k_la_tokens<T, 64>, grid, block, s, w);
-    return launch(k_la_tokens<T, 128>, grid, block, s, w);
-}
-
-hipError_t launch_la_walk(const LaWalk& w, int act, void*, hipStream_t s) {
-    return act == SSD_BF16 ? walk_t<bf16>(w, s) : walk_t<float>(w, s);
+hipError_t launch_la_walk(const LaWalk& w, int act, void* ws, hipStream_t s) {
+    return act == SSD_BF16 ? walk_t<bf16>(w, ws, s) : walk_t<float>(w, ws, s);
 }
 
 hipError_t launch_la_group_sum(const LaWalk& w, int act, const float* part, int nkv, void* out,

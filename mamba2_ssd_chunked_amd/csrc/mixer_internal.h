@@ -53,12 +53,6 @@ __device__ __forceinline__ SeqRange seq_range(const LaWalk& w, int s) {
     return r;
 }
 
-// l^e for e >= 0, with l^0 = 1 also for l = 0 (log2 decay of minus infinity).
-__device__ __forceinline__ float decay_pow(float l2, int e) {
-    return e == 0 ? 1.f : __builtin_amdgcn_exp2f(l2 * (float)e);
-}
-constexpr float LOG2E = 1.4426950408889634f;
-
 size_t la_walk_ws(const LaWalk& w, int act);
 hipError_t launch_la_walk(const LaWalk& w, int act, void* ws, hipStream_t s);
 // out[t][hk][d] = sum over the group's heads of part[t][h][d], tokens of sequences only
