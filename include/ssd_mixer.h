@@ -56,7 +56,7 @@ typedef struct {
     int64_t dq_stride, dk_stride, dv_stride;
 } ssd_linattn;
 /* Size limits (SSD_ERR_SHAPE beyond them): batch * seqlen <= 2^31 - 1 tokens,
- * nheads <= 65535, sequences <= 2^24, token strides below 2^24 elements, and every
+ * nheads <= 65535, sequences <= 2^24, token strides below 2^23 elements, and every
  * launch grid within the hardware's limits. */
 
 /* Bytes of workspace for the forward (SSD_WS_FORWARD) or backward (SSD_WS_BACKWARD)

@@ -6,8 +6,10 @@
 // state that enters it:
 //   out_i = inter l^(i+1) M a_i + intra sum_{j<=i} l^(i-j) (b_j . a_i) c_j
 //   M     <- l^n M + s sum_j l^(n-1-j) c_j b_j^T
-// so the work is three matrix products per chunk, and M never leaves the registers: wave w
-// of the workgroup keeps columns w CD/4 .. of M^T [BD][CD] in float32 accumulators.
+// so the work is three matrix products per chunk, and M never leaves the registers: a
+// workgroup has 64 columns of M^T [BD][CD], each of its four waves 16 of them in float32
+// accumulators.  (Where CD is 128, two neighbouring workgroups form the same scores and read
+// the same a and b, the second time from L2.)
 //
 // A sequence is walked by as many workgroups as it has spans of `span` tokens (LaPlan).
 // Where a sequence has more than one, a first launch (OUT = false) leaves the state that
@@ -85,7 +87,10 @@ __device__ __forceinline__ LaSpan la_span(const LaWalk& w, const LaPlan& p, int6
 }
 
 // Rows of one operand on their way into LDS: 16-byte vectors of D channels per token.
-template <typename T, int D>
+// They come through bounded buffer loads, which give zeros for rows without a token and
+// need no branch or select: the n tokens of a last chunk take its last rows, so that the
+// weights l^(Q-1-j) of its rows are every chunk's.
+template <typename T, int D, bool REV>
 struct LaRows {
     static constexpr int Q = LaCfg<T>::Q, VEC = 16 / (int)sizeof(T), VPR = D / VEC;
     static constexpr int RPP = 256 / VPR, NP = Q / RPP;  // rows per pass, passes
@@ -93,17 +98,16 @@ struct LaRows {
     typedef T vt __attribute__((ext_vector_type(VEC)));
     vt v[NP];
 
-    // rows of the n tokens from t0 (in memory order), visited backwards if `rev`; rows
-    // behind them are zero
-    __device__ __forceinline__ void load(const T* base, int64_t ts, int64_t t0, int n, bool rev) {
-        const T* p = base + t0 * ts;
-        const int r0 = threadIdx.x / VPR, c = (threadIdx.x % VPR) * VEC;
+    // rows of the n tokens from t0 (in memory order), `ts` elements apart, visited backwards
+    // if REV; a row without a token is beyond the bound (forwards by its negative offset)
+    __device__ __forceinline__ void load(const T* base, int ts, int64_t t0, int n) {
+        const int bytes = ts * (int)sizeof(T);
+        const __amdgpu_buffer_rsrc_t r = buf_rsrc(base + t0 * ts, n * bytes);
+        const int r0 = threadIdx.x / VPR, c = (threadIdx.x % VPR) * 16;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int r = r0 + i * RPP;
-            const int row = r < n ? (rev ? n - 1 - r : r) : 0;
-            v[i] = *(const vt*)at32(p, (uint32_t)row * (uint32_t)ts + c);
-            if (r >= n) v[i] = vt{};
+            const int row = r0 + i * RPP;
+            v[i] = buf_load<vt>(r, (REV ? Q - 1 - row : row - (Q - n)) * bytes + c);
         }
     }
     __device__ __forceinline__ void store(T* lds) const {
@@ -164,31 +168,37 @@ __device__ __forceinline__ float la_pow(double l2, int e) {
     return e == 0 ? 1.f : __builtin_amdgcn_exp2f((float)(l2 * (double)e));
 }
 
-template <typename T, int BD, int CD, bool OUT>
+enum LaOut { LA_STATE = 0, LA_ACT = 1, LA_F32 = 2 };  // what a walk leaves behind
+
+template <typename T, int BD, int OUT>
 constexpr int la_lds_bytes() {
     constexpr int Q = LaCfg<T>::Q, V = 16 / (int)sizeof(T), NT = Q / 16;
-    return Q * (BD + V) * (int)sizeof(T) * (OUT ? 2 : 1) + Q * (CD + V) * (int)sizeof(T) +
+    return Q * (BD + V) * (int)sizeof(T) * (OUT ? 2 : 1) + Q * (64 + V) * (int)sizeof(T) +
            (OUT ? NT * (NT / LaCfg<T>::TPK) * 1024 : 0);
 }
 
-// Workgroup of four waves per (span, head).  SPLITS: bf16 terms per weighted c (1 for
-// float32).  `ws`: the spans' states, [slot][H][wave][tile][lane] f32x4.
-template <typename T, int BD, int CD, bool OUT, int SPLITS>
-__global__ void __launch_bounds__(256, 2) k_la_walk(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
+// Workgroup of four waves per (span, head, 64 columns).  SPLITS: bf16 terms per weighted c
+// (1 for float32).  `ws`: the spans' states, [slot][H][CD / 64][wave][tile][lane] f32x4.
+template <typename T, int BD, bool REV, int OUT, int SPLITS>
+__global__ void __launch_bounds__(256, BD == 64 ? 3 : 2) k_la_walk(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
     typedef Mma<T> M;
     typedef typename M::Frag Frag;
     constexpr int Q = LaCfg<T>::Q, TPK = LaCfg<T>::TPK, NT = Q / 16, NK = NT / TPK;
     constexpr int SL = M::SL, KS = M::KS, KB = BD / KS;
-    constexpr int BT = BD / 16, CW = CD / 4, CT = CW / 16;  // tiles of M^T of one wave
-    constexpr int AP = LaRows<T, BD>::PITCH, CP = LaRows<T, CD>::PITCH;
-    __shared__ __align__(16) unsigned char lds[la_lds_bytes<T, BD, CD, OUT>()];
+    constexpr int BT = BD / 16;  // tiles of M^T of one wave
+    constexpr int AP = LaRows<T, BD, REV>::PITCH, CP = LaRows<T, 64, REV>::PITCH;
+    __shared__ __align__(16) unsigned char lds[la_lds_bytes<T, BD, OUT>()];
     T* sb = (T*)lds;
     T* sc = sb + Q * AP;
     T* sa = sc + Q * CP;
     Frag* sp = (Frag*)(sa + Q * AP);  // scores, [row tile][k block][lane]
 
+    // consecutive items (the column halves and heads that share rows) go to one XCD
     const int64_t nblk = gridDim.x;
-    const int64_t item = nblk % 8 == 0 ? (blockIdx.x % 8) * (nblk / 8) + blockIdx.x / 8 : blockIdx.x;
+    int64_t item = nblk % 8 == 0 ? (blockIdx.x % 8) * (nblk / 8) + blockIdx.x / 8 : blockIdx.x;
+    const int CD = w.cd, nct = CD / 64;
+    const int ct = (int)(item % nct);
+    item /= nct;
     const int h = (int)(item % w.H);
     const int64_t slot = item / w.H;
     const LaSpan sp_ = la_span(w, plan, slot);
@@ -196,58 +206,57 @@ __global__ void __launch_bounds__(256, 2) k_la_walk(LaWalk w, LaPlan plan, f32x4
     const int wave = wave_id(), lane = threadIdx.x % 64, lr = lane % 16, lg = lane / 16;
     const T* pa = (const T*)w.a + (int64_t)(h / w.a_div) * BD;
     const T* pb = (const T*)w.b + (int64_t)(h / w.b_div) * BD;
-    const T* pc = (const T*)w.c + (int64_t)(h / w.c_div) * CD;
-    const int64_t state_at = ((int64_t)sp_.s * w.H + h) * (BD * CD);
-    f32x4* mine = ws + (((slot * w.H + h) * 4 + wave) * (BT * CT)) * 64 + lane;
-
+    const T* pc = (const T*)w.c + (int64_t)(h / w.c_div) * CD + ct * 64;
+    const int ats = (int)w.a_ts, bts = (int)w.b_ts, cts = (int)w.c_ts;
     const int nch = (sp_.n + Q - 1) / Q;
+
     // tokens of chunk k in memory order: [t0, t0 + n)
     auto first_token = [&](int k, int n) {
         const int64_t i = sp_.i0 + (int64_t)k * Q;
-        return w.reverse ? sp_.hi - i - n : sp_.lo + i;
+        return REV ? sp_.hi - i - n : sp_.lo + i;
     };
     auto tokens_of = [&](int k) { return sp_.n - k * Q < Q ? sp_.n - k * Q : Q; };
-    LaRows<T, BD> ra, rb;
-    LaRows<T, CD> rc;
+    LaRows<T, BD, REV> ra, rb;
+    LaRows<T, 64, REV> rc;
     auto load = [&](int k) {
         const int n = tokens_of(k);
         const int64_t t0 = first_token(k, n);
-        if constexpr (OUT) ra.load(pa, w.a_ts, t0, n, w.reverse);
-        rb.load(pb, w.b_ts, t0, n, w.reverse);
-        rc.load(pc, w.c_ts, t0, n, w.reverse);
+        rb.load(pb, bts, t0, n);
+        rc.load(pc, cts, t0, n);
+        if constexpr (OUT) ra.load(pa, ats, t0, n);
     };
     if (nch > 0) load(0);
 
-    // the state that enters the span
-    f32x4 St[BT][CT];
+    // the state that enters the span; this lane's elements of tile t are channels
+    // 16 t + 4 lg .. of b and channel `col` of c
+    f32x4 St[BT];
+    const int col = ct * 64 + wave * 16 + lr;
     const bool given = sp_.j == 0;
+    f32x4* mine = ws + (((slot * w.H + h) * nct + ct) * 4 + wave) * (BT * 64) + lane;
+    const int64_t state_at = ((int64_t)sp_.s * w.H + h) * ((int64_t)BD * CD) +
+                             (w.trans ? (int64_t)4 * lg * CD + col : (int64_t)col * BD + 4 * lg);
+    if (OUT && !given) {
 #pragma unroll
-    for (int t = 0; t < BT; ++t)
+        for (int t = 0; t < BT; ++t) St[t] = mine[t * 64];
+    } else if (given && w.init && !w.trans) {
 #pragma unroll
-        for (int u = 0; u < CT; ++u) {
-            const int bd = 16 * t + 4 * lg, cd = wave * CW + 16 * u + lr;
-            f32x4 v = {0.f, 0.f, 0.f, 0.f};
-            if (given) {
-                if (w.init) {
-                    const float* p = w.init + state_at;
-                    if (w.trans) {
+        for (int t = 0; t < BT; ++t) St[t] = *(const f32x4*)(w.init + state_at + 16 * t);
+    } else if (given && w.init) {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) v[r] = p[(bd + r) * CD + cd];
-                    } else {
-                        v = *(const f32x4*)(p + cd * BD + bd);
-                    }
-                }
-            } else if constexpr (OUT) {
-                v = mine[(t * CT + u) * 64];
-            }
-            St[t][u] = v;
-        }
+        for (int t = 0; t < BT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) St[t][r] = w.init[state_at + (int64_t)(16 * t + r) * CD];
+    } else {
+#pragma unroll
+        for (int t = 0; t < BT; ++t) St[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 
     const float ld = w.log_decay[h];
     const double l2 = (double)ld * 1.4426950408889634;
     // l^(i - j) of a lane's four j in the diagonal score tile, and l^(16 + i - j) for the
     // tiles below it, whose further factor l^(16 (d - 1)) the whole wave shares
-    float dg[4], lw[4], far[NT > 2 ? NT - 2 : 1];
+    float dg[4], lw[4];
+    const float l16 = la_pow(l2, 16), l32 = la_pow(l2, 32);
     if constexpr (OUT) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -255,37 +264,46 @@ __global__ void __launch_bounds__(256, 2) k_la_walk(LaWalk w, LaPlan plan, f32x4
             dg[r] = w.intra * la_pow(l2, d > 0 ? d : 0);
             lw[r] = w.intra * la_pow(l2, 16 + d);
         }
-#pragma unroll
-        for (int d = 0; d < (NT > 2 ? NT - 2 : 1); ++d) far[d] = la_pow(l2, 16 * (d + 1));
     }
-    const float lq = (float)exp((double)Q * (double)ld);  // compounded per chunk: exact to 2^-25
-    float wk[NK][SL];  // s l^(n-1-j) of the lane's k slots
-    auto weights = [&](int n) {
+    float wk[NK][SL];  // s l^(Q-1-j) of the lane's k slots
 #pragma unroll
-        for (int k = 0; k < NK; ++k)
+    for (int k = 0; k < NK; ++k)
 #pragma unroll
-            for (int s = 0; s < SL; ++s) {
-                const int j = KS * k + 16 * (s / 4) + 4 * lg + s % 4;
-                wk[k][s] = j < n ? w.state_scale * la_pow(l2, n - 1 - j) : 0.f;
-            }
-    };
-    weights(Q);
+        for (int s = 0; s < SL; ++s)
+            wk[k][s] = w.state_scale *
+                       la_pow(l2, Q - 1 - (KS * k + 16 * (s / 4) + 4 * lg + s % 4));
+    // The given state of a REV walk is not decayed before its first use.
+    const bool late = REV && given;
+    // l^n, compounded from chunk to chunk: the exact power, rounded once
+    auto power = [&](int e) { return e == 0 ? 1.f : (float)exp((double)e * (double)ld); };
+    const int nlast = sp_.n - (nch - 1) * Q;
+    const float lq = power(Q), lfirst = late ? power(Q - 1) : lq,
+                llast = power(late && nch == 1 ? nlast - 1 : nlast);
     float row[NT];  // inter l^(i+1)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) row[t] = w.inter * la_pow(l2, 16 * t + lr + 1);
+    for (int t = 0; t < NT; ++t) row[t] = w.inter * la_pow(l2, 16 * t + lr + (late ? 0 : 1));
+    const float l1 = la_pow(l2, 1);
+    const int out_bytes = (int)w.out_ts * (OUT == LA_F32 ? 4 : (int)sizeof(T));
 
     for (int k = 0; k < nch; ++k) {
         const int n = tokens_of(k);
-        const bool late = w.reverse && given && k == 0;  // the given state is not decayed yet
         __syncthreads();  // the last chunk's reads are done
-        if constexpr (OUT) ra.store_k(sa);
         rb.store_k(sb);
         rc.store(sc);
+        if constexpr (OUT) ra.store_k(sa);
         __syncthreads();
-        if (k + 1 < nch) load(k + 1);
-        if (n != Q) weights(n);
+        // the last chunk's prefetch repeats it: no branch, so no full waits at a join
+        load(k + 1 < nch ? k + 1 : k);
+        const float keep = k + 1 == nch ? llast : (k == 0 ? lfirst : lq);
+        if (OUT && n != Q) {  // the last chunk's tokens begin at row Q - n
+            int i0 = lr - (Q - n) + (late && k == 0 ? 0 : 1);
+            asm volatile("" : "+v"(i0));  // computed here, not held from before the loop
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                row[t] = w.inter * la_pow(l2, 16 * t + i0 > 0 ? 16 * t + i0 : 0);
+        }
 
-        f32x4 o[NT][CT];
+        f32x4 o[NT];
         if constexpr (OUT) {
             // scores of row tile `wave`: k blocks up to the diagonal
             if (wave < NT) {
@@ -295,6 +313,7 @@ __global__ void __launch_bounds__(256, 2) k_la_walk(LaWalk w, LaPlan plan, f32x4
                     af[q] = M::load(sa + (16 * wave + lr) * AP + KS * q + SL * lg);
 #pragma unroll
                 for (int kb = 0; kb < NK; ++kb) {
+                    if (kb * TPK > wave) break;
                     f32x4 tl[TPK];
 #pragma unroll
                     for (int e = 0; e < TPK; ++e) {
@@ -310,8 +329,7 @@ __global__ void __launch_bounds__(256, 2) k_la_walk(LaWalk w, LaPlan plan, f32x4
                                 for (int r = 0; r < 4; ++r)
                                     acc[r] = 4 * lg + r <= lr ? acc[r] * dg[r] : 0.f;
                             } else {
-                                const int d = wave - jt;
-                                const float f = d == 1 ? 1.f : far[d - 2 < NT - 2 ? d - 2 : 0];
+                                const float f = wave - jt == 1 ? 1.f : (wave - jt == 2 ? l16 : l32);
 #pragma unroll
                                 for (int r = 0; r < 4; ++r) acc[r] *= lw[r] * f;
                             }
@@ -321,176 +339,131 @@ __global__ void __launch_bounds__(256, 2) k_la_walk(LaWalk w, LaPlan plan, f32x4
                     sp[(wave * NK + kb) * 64 + lane] = la_frag<T>(tl);
                 }
             }
-            // M a_i
+            // l^(i+1) M a_i
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int u = 0; u < CT; ++u) o[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < NT; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < KB; ++q) {
-                Frag sf[CT];
+                const Frag sf = la_frag<T>(&St[q * TPK]);
 #pragma unroll
-                for (int u = 0; u < CT; ++u) {
-                    f32x4 tl[TPK];
-#pragma unroll
-                    for (int e = 0; e < TPK; ++e) tl[e] = St[q * TPK + e][u];
-                    sf[u] = la_frag<T>(tl);
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const Frag a = M::load(sa + (16 * t + lr) * AP + KS * q + SL * lg);
-#pragma unroll
-                    for (int u = 0; u < CT; ++u) o[t][u] = M::mma(sf[u], a, o[t][u]);
-                }
+                for (int t = 0; t < NT; ++t)
+                    o[t] = M::mma(sf, M::load(sa + (16 * t + lr) * AP + KS * q + SL * lg), o[t]);
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float f = late ? w.inter * la_pow(l2, 16 * t + lr) : row[t];
-#pragma unroll
-                for (int u = 0; u < CT; ++u) o[t][u] *= f;
-            }
+            for (int t = 0; t < NT; ++t) o[t] *= row[t];
             __syncthreads();  // the scores are there
         }
 
-        Frag cf[NK][CT];
+        Frag cf[NK];
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) cf[kb] = XT<T>::load(sc, CP, KS * kb, wave * 16, lane);
+        // w_j c_j, and whether one of this wave's c is not finite
+        float x[NK][SL], all = 0.f;
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
-            for (int u = 0; u < CT; ++u)
-                cf[kb][u] = XT<T>::load(sc, CP, KS * kb, wave * CW + 16 * u, lane);
-        if constexpr (OUT) {
-            bool wild = false;  // a sum is not finite
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                for (int kb = 0; kb <= t / TPK; ++kb) {
-                    const Frag p = sp[(t * NK + kb) * 64 + lane];
-#pragma unroll
-                    for (int u = 0; u < CT; ++u) o[t][u] = M::mma(cf[kb][u], p, o[t][u]);
-                }
-#pragma unroll
-                for (int u = 0; u < CT; ++u) {
-                    const f32x4 v = o[t][u];
-                    wild = wild || !(fabsf((v[0] + v[1]) + (v[2] + v[3])) < INFINITY);
-                }
+            for (int s = 0; s < SL; ++s) {
+                x[kb][s] = (float)cf[kb][s] * wk[kb][s];
+                all += x[kb][s];
             }
-            if (__ballot(wild)) {
-                // A c_j that is not finite times a masked score's 0 is NaN in the outputs
-                // before j too.  Row by row, with the later c taken out, it is not.
+        if constexpr (OUT) {
+            // A c_j that is not finite times a masked score's 0 would be NaN in the outputs
+            // before j too.  It is taken out of the product, and the outputs of its channel
+            // from j on are set.
+            const bool wild = __ballot(!(fabsf(all) < INFINITY)) != 0;
+            int from[4];
+            if (wild) {
+                int j0 = Q;
+                int g4 = 4 * lg;
+                asm volatile("" : "+v"(g4));
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    f32x4 base[CT];
+                for (int kb = NK - 1; kb >= 0; --kb)
 #pragma unroll
-                    for (int u = 0; u < CT; ++u) base[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int q = 0; q < KB; ++q)
-#pragma unroll
-                        for (int u = 0; u < CT; ++u) {
-                            f32x4 tl[TPK];
-#pragma unroll
-                            for (int e = 0; e < TPK; ++e) tl[e] = St[q * TPK + e][u];
-                            base[u] = M::mma(la_frag<T>(tl),
-                                             M::load(sa + (16 * t + lr) * AP + KS * q + SL * lg),
-                                             base[u]);
+                    for (int s = SL - 1; s >= 0; --s)
+                        if (!(fabsf((float)cf[kb][s]) < INFINITY)) {
+                            j0 = KS * kb + 16 * (s / 4) + s % 4 + g4;
+                            cf[kb][s] = (T)0.f;
                         }
-                    const float f = late ? w.inter * la_pow(l2, 16 * t + lr) : row[t];
-                    for (int i = 0; i < 16; ++i)
+                j0 = min(j0, __shfl_xor(j0, 16, 64));
+                j0 = min(j0, __shfl_xor(j0, 32, 64));
 #pragma unroll
-                        for (int u = 0; u < CT; ++u) {
-                            f32x4 v = base[u] * f;
+                for (int r = 0; r < 4; ++r) from[r] = __shfl(j0, 4 * lg + r, 64);
+            }
 #pragma unroll
-                            for (int kb = 0; kb <= t / TPK; ++kb) {
-                                Frag c = cf[kb][u];
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                                for (int s = 0; s < SL; ++s)
-                                    if (KS * kb + 16 * (s / 4) + 4 * lg + s % 4 > 16 * t + i)
-                                        c[s] = (T)0.f;
-                                v = M::mma(c, sp[(t * NK + kb) * 64 + lane], v);
-                            }
-                            if (lr == i) o[t][u] = v;
-                        }
-                }
+                for (int kb = 0; kb <= t / TPK; ++kb)
+                    o[t] = M::mma(cf[kb], sp[(t * NK + kb) * 64 + lane], o[t]);
+            if (wild) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * t + lr >= from[r]) o[t][r] = NAN;
             }
         }
 
         // M <- l^n M + b^T (w c)
-        const float keep = late ? (float)exp((double)(n - 1) * (n > 1 ? (double)ld : 0.0))
-                                : (n == Q ? lq : (float)exp((double)n * (double)ld));
 #pragma unroll
-        for (int t = 0; t < BT; ++t)
-#pragma unroll
-            for (int u = 0; u < CT; ++u) St[t][u] *= keep;
+        for (int t = 0; t < BT; ++t) St[t] *= keep;
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
-            Frag wc[SPLITS][CT];
+            Frag wc[SPLITS];
 #pragma unroll
-            for (int u = 0; u < CT; ++u)
+            for (int s = 0; s < SL; ++s) {
 #pragma unroll
-                for (int s = 0; s < SL; ++s) {
-                    float x = (float)cf[kb][u][s] * wk[kb][s];
-#pragma unroll
-                    for (int p = 0; p < SPLITS; ++p) {
-                        wc[p][u][s] = (T)x;
-                        x -= (float)wc[p][u][s];
-                    }
+                for (int p = 0; p < SPLITS; ++p) {
+                    wc[p][s] = (T)x[kb][s];
+                    x[kb][s] -= (float)wc[p][s];
                 }
+            }
 #pragma unroll
             for (int t = 0; t < BT; ++t) {
                 const Frag bt = la_bt<T>(sb, AP, KS * kb, t, lane);
 #pragma unroll
-                for (int u = 0; u < CT; ++u)
-#pragma unroll
-                    for (int p = SPLITS - 1; p >= 0; --p)
-                        St[t][u] = M::mma(bt, wc[p][u], St[t][u]);
+                for (int p = SPLITS - 1; p >= 0; --p) St[t] = M::mma(bt, wc[p], St[t]);
             }
         }
 
         if constexpr (OUT) {
-            // a lane holds channels 4 lg .. of token lr of every tile
-            const int64_t t0 = first_token(k, n);
+            // a lane holds channels 4 lg .. of row lr of every tile; rows without a token are
+            // beyond the buffer's bound
+            typedef typename std::conditional<OUT == LA_F32, float, T>::type OT;
+            typedef typename Vec4<OT>::type ov;
+            const __amdgpu_buffer_rsrc_t r =
+                buf_rsrc((OT*)w.out + first_token(k, n) * w.out_ts + (int64_t)h * CD + ct * 64,
+                         n * out_bytes);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int i = 16 * t + lr;
-                if (i < n) {
-                    const int64_t tok = t0 + (w.reverse ? n - 1 - i : i);
-                    const int64_t at = tok * w.out_ts + (int64_t)h * CD + wave * CW + 4 * lg;
+                ov v;
 #pragma unroll
-                    for (int u = 0; u < CT; ++u) {
-                        if (w.out_f32) {
-                            *(f32x4*)((float*)w.out + at + 16 * u) = o[t][u];
-                        } else {
-                            typename Vec4<T>::type v;
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) v[r] = (T)o[t][u][r];
-                            *(typename Vec4<T>::type*)((T*)w.out + at + 16 * u) = v;
-                        }
-                    }
-                }
+                for (int c = 0; c < 4; ++c) v[c] = (OT)o[t][c];
+                buf_store(v, r, (REV ? Q - 1 - i : i - (Q - n)) * out_bytes +
+                                    (wave * 16 + 4 * lg) * (int)sizeof(OT));
             }
+        }
+        if (late && k == 0) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) row[t] *= l1;
         }
     }
 
     if constexpr (!OUT) {
 #pragma unroll
-        for (int t = 0; t < BT; ++t)
-#pragma unroll
-            for (int u = 0; u < CT; ++u) mine[(t * CT + u) * 64] = St[t][u];
+        for (int t = 0; t < BT; ++t) mine[t * 64] = St[t];
     } else if (w.fin && sp_.last) {
-        const float keep = w.reverse && sp_.n > 0 ? (float)exp((double)ld) : 1.f;
+        const float keep = REV && sp_.n > 0 ? (float)exp((double)ld) : 1.f;
 #pragma unroll
-        for (int t = 0; t < BT; ++t)
+        for (int t = 0; t < BT; ++t) {
+            const f32x4 v = St[t] * keep;
+            if (w.trans) {
 #pragma unroll
-            for (int u = 0; u < CT; ++u) {
-                const int bd = 16 * t + 4 * lg, cd = wave * CW + 16 * u + lr;
-                float* p = w.fin + state_at;
-                const f32x4 v = St[t][u] * keep;
-                if (w.trans) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) p[(bd + r) * CD + cd] = v[r];
-                } else {
-                    *(f32x4*)(p + cd * BD + bd) = v;
-                }
+                for (int r = 0; r < 4; ++r) w.fin[state_at + (int64_t)(16 * t + r) * CD] = v[r];
+            } else {
+                *(f32x4*)(w.fin + state_at + 16 * t) = v;
             }
+        }
     }
 }
 

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(256) k_la_group_sum(LaWalk w, const float* __r
 constexpr int LA_BLOCKS = 512, LA_MIN_SPAN = 256;
 
 static LaPlan la_plan(const LaWalk& w) {
-    const int64_t per = (w.tokens * w.H + LA_BLOCKS - 1) / LA_BLOCKS;
+    const int64_t per = (w.tokens * w.H * (w.cd / 64) + LA_BLOCKS - 1) / LA_BLOCKS;
     LaPlan p;
     p.span = (int)((per > LA_MIN_SPAN ? per + 63 : LA_MIN_SPAN) / 64 * 64);
     p.slots = w.tokens / p.span + w.nseq;
@@ -62,28 +62,33 @@ size_t la_walk_ws(const LaWalk& w, int) {
     return p.split ? (size_t)p.slots * w.H * w.bd * w.cd * 4 : 0;
 }
 
-template <typename T, int BD, int CD>
+template <typename T, int BD, bool REV>
 static hipError_t walk_shape(const LaWalk& w, f32x4* ws, hipStream_t s) {
-    constexpr bool B16 = sizeof(T) == 2;
+    constexpr int FINE = sizeof(T) == 2 ? 3 : 1, FAST = sizeof(T) == 2 ? 2 : 1;
     const LaPlan p = la_plan(w);
-    const dim3 grid((unsigned)(p.slots * w.H)), block(256);
+    const dim3 grid((unsigned)(p.slots * w.H * (w.cd / 64))), block(256);
     if (p.split) {
-        SSD_TRY(launch(k_la_walk<T, BD, CD, false, B16 ? 3 : 1>, grid, block, s, w, p, ws));
-        constexpr int quads = BD * CD / 4;
+        SSD_TRY(launch(k_la_walk<T, BD, REV, LA_STATE, FINE>, grid, block, s, w, p, ws));
+        const int quads = BD * w.cd / 4;
         SSD_TRY(launch(k_la_spans, dim3((unsigned)((int64_t)w.nseq * w.H * (quads / 256))),
                        dim3(256), s, w, p, quads, ws));
     }
-    if (B16 && !w.fin) return launch(k_la_walk<T, BD, CD, true, B16 ? 2 : 1>, grid, block, s, w, p, ws);
-    return launch(k_la_walk<T, BD, CD, true, B16 ? 3 : 1>, grid, block, s, w, p, ws);
+    if constexpr (REV)
+        if (w.out_f32) {
+            if (w.fin) return launch(k_la_walk<T, BD, REV, LA_F32, FINE>, grid, block, s, w, p, ws);
+            return launch(k_la_walk<T, BD, REV, LA_F32, FAST>, grid, block, s, w, p, ws);
+        }
+    if (w.fin) return launch(k_la_walk<T, BD, REV, LA_ACT, FINE>, grid, block, s, w, p, ws);
+    return launch(k_la_walk<T, BD, REV, LA_ACT, FAST>, grid, block, s, w, p, ws);
 }
 
 template <typename T>
 static hipError_t walk_t(const LaWalk& w, void* ws, hipStream_t s) {
-    if (w.bd == 64 && w.cd == 64) return walk_shape<T, 64, 64>(w, (f32x4*)ws, s);
-    if (w.bd == 64 && w.cd == 128) return walk_shape<T, 64, 128>(w, (f32x4*)ws, s);
-    if (w.bd == 128 && w.cd == 64) return walk_shape<T, 128, 64>(w, (f32x4*)ws, s);
-    if (w.bd == 128 && w.cd == 128) return walk_shape<T, 128, 128>(w, (f32x4*)ws, s);
-    return hipErrorInvalidValue;
+    if (w.bd == 64)
+        return w.reverse ? walk_shape<T, 64, true>(w, (f32x4*)ws, s)
+                         : walk_shape<T, 64, false>(w, (f32x4*)ws, s);
+    return w.reverse ? walk_shape<T, 128, true>(w, (f32x4*)ws, s)
+                     : walk_shape<T, 128, false>(w, (f32x4*)ws, s);
 }
 
 bool la_supported(int keydim, int valdim, int act) {

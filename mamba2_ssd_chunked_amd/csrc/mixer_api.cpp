@@ -34,7 +34,7 @@ int check_linattn(const ssd_linattn* p, LaStrides* st) {
     const int64_t esz = p->act_dtype == SSD_BF16 ? 2 : 4;
     auto stride = [&](int64_t given, int64_t packed, int64_t* out) {
         *out = given == 0 ? packed : given;
-        if (*out < packed || *out >= (1ll << 24)) return (int)SSD_ERR_SHAPE;
+        if (*out < packed || *out >= (1ll << 23)) return (int)SSD_ERR_SHAPE;
         return *out * esz % 16 == 0 ? (int)SSD_OK : (int)SSD_ERR_ALIGN;
     };
     const int64_t H = p->nheads, K = p->nkvheads, Dk = p->keydim, Dv = p->valdim;
@@ -145,12 +145,12 @@ size_t linattn_ws(const ssd_linattn* p, const LaStrides& st, int32_t nseq, int32
     return part_bytes(p) + n;
 }
 
-// Every launch of the walks fits: a workgroup per (span, head), spans of at least 256
-// tokens, and up to 16 per (sequence, head) to compose span states.
+// Every launch of the walks fits: up to two workgroups per (span, head), spans of at least
+// 256 tokens, and up to 16 per (sequence, head) to compose span states.
 int check_walk_grid(const ssd_linattn* p, int32_t nseq) {
     typedef unsigned __int128 u128;
     const u128 spans = (u128)(p->batch * p->seqlen) / 256 + nseq;
-    const u128 blocks = (spans > (u128)nseq * 16 ? spans : (u128)nseq * 16) * p->nheads;
+    const u128 blocks = (2 * spans > (u128)nseq * 16 ? 2 * spans : (u128)nseq * 16) * p->nheads;
     return blocks <= (u128)MAX_BLOCKS ? SSD_OK : SSD_ERR_SHAPE;
 }
 
