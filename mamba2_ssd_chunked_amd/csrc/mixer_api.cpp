@@ -349,7 +349,7 @@ int ssd_norm_fwd(const ssd_norm* problem, const void* x, const void* z, const fl
 size_t ssd_norm_workspace_bytes(const ssd_norm* problem) {
     NormArgs a = {};
     if (check_norm(problem, &a) != SSD_OK) return 0;
-    return (size_t)norm_row_blocks(a, problem->act_dtype) * 2 * a.C * 4;
+    return norm_bwd_ws(a, problem->act_dtype);
 }
 
 int ssd_norm_bwd(const ssd_norm* problem, const void* x, const void* z, const float* weight,

@@ -6,6 +6,19 @@
 
 namespace ssd {
 
+// Launch with `lds` bytes of dynamic LDS (see launch).
+template <typename... KArgs, typename... Args>
+inline hipError_t launch_lds(void (*kernel)(KArgs...), dim3 grid, dim3 block, int lds, hipStream_t s,
+                             Args&&... args) {
+    std::tuple<KArgs...> a(std::forward<Args>(args)...);
+    return std::apply(
+        [&](auto&... v) {
+            std::array<void*, sizeof...(KArgs) + 1> p = {(void*)&v..., nullptr};
+            return hipLaunchKernel((const void*)kernel, grid, block, p.data(), lds, s);
+        },
+        a);
+}
+
 // ---- linear attention ------------------------------------------------------------
 //
 // Forward and backward are the same walk over a sequence with its operands in other
@@ -101,9 +114,8 @@ struct NormArgs {
     int mode, center;
     float eps;
 };
-// row blocks of the backward: the rows of one group are dealt out to this many
-// workgroups, each of which leaves partial sums of dweight and dbias
-int norm_row_blocks(const NormArgs& a, int act);
+// bytes of the backward's partial sums of dweight and dbias
+size_t norm_bwd_ws(const NormArgs& a, int act);
 hipError_t launch_norm_fwd(const NormArgs& a, int act, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, int act, float* part, hipStream_t s);
 

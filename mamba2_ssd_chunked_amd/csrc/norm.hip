@@ -5,6 +5,12 @@
 //   y = lin, silu(lin) or lin s
 // Backward, with e the gradient that reaches lin, g = e w:
 //   du = r (g - [center] mean(g) - n mean(g n));  dw = sum e n, db = sum e.
+//
+// Bound by HBM: x, z (and dy) read once, y (dx, dz) written once.  A group of a row is held
+// in registers by a team of lanes between its statistics and its outputs; a team keeps one
+// group for all its rows, so that weight and bias, and the sums of dweight and dbias, stay
+// in registers too.  Groups too wide for a team, or not in whole 16-byte vectors, take the
+// kernels that read a group again for every sweep (k_norm_*_any).
 #include "mixer_internal.h"
 
 namespace ssd {
@@ -142,42 +148,444 @@ __global__ void __launch_bounds__(256) k_norm_bwd_any(NormArgs a, float* __restr
     }
 }
 
-// dw and db from the blocks' partial sums, in the blocks' order.
-__global__ void __launch_bounds__(256) k_norm_reduce(const float* __restrict__ part, int blocks,
-                                                    int C, float* __restrict__ dw,
-                                                    float* __restrict__ db) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= C) return;
-    float sw = 0.f, sb = 0.f;
-    for (int i = 0; i < blocks; ++i) {
-        sw += part[(int64_t)i * 2 * C + c];
-        sb += part[(int64_t)i * 2 * C + C + c];
+// ---- teams --------------------------------------------------------------------------
+//
+// A team of `lpt` neighbouring lanes of a workgroup (a power of two; with WIDE several
+// waves), holds EPL channels to a lane: vectors lane, lane + lpt, ... of the group.
+
+constexpr int NORM_NT = 512;
+
+template <typename T>
+struct NormVec {
+    static constexpr int E = 16 / (int)sizeof(T);
+    typedef T type __attribute__((ext_vector_type(E)));
+};
+
+// Team sums of N values at once.  With WIDE every team of the workgroup calls it.
+template <int N, bool WIDE>
+__device__ __forceinline__ void team_sum(float (&v)[N], int lpt, float (*red)[NORM_NT / 64]) {
+    for (int o = 1; o < (WIDE ? 64 : lpt); o <<= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o, 64);
+    if constexpr (WIDE) {
+        __syncthreads();  // the last sums have been read
+        if (threadIdx.x % 64 == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) red[i][threadIdx.x / 64] = v[i];
+        __syncthreads();
+        const int w0 = threadIdx.x / lpt * (lpt / 64);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.f;
+        for (int k = 0; k < lpt / 64; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += red[i][w0 + k];
     }
-    dw[c] = sw;
-    if (db) db[c] = sb;
 }
 
-int norm_row_blocks(const NormArgs& a, int) {
-    const int64_t want = 1024 / a.G < 1 ? 1 : 1024 / a.G;
-    return (int)(a.rows < want ? a.rows : want);
+// The same vector as far as the compiler knows anew: what was computed from it before is
+// computed again, not held.
+template <typename V>
+__device__ __forceinline__ V forget(V v) {
+    f32x4 h = __builtin_bit_cast(f32x4, v);
+    asm volatile("" : "+v"(h));
+    return __builtin_bit_cast(V, h);
+}
+
+struct NormTeam {
+    int lane, lpt;       // place in the team, its lanes
+    int64_t item, step;  // first (row, group), distance to the next
+    int c0, nv;          // the group's first channel and its vectors
+    int turns;           // (row, group)s of the team, with WIDE of the workgroup's busiest
+};
+template <typename T, bool WIDE>
+__device__ __forceinline__ NormTeam norm_team(const NormArgs& a, int lpt) {
+    NormTeam t;
+    t.lpt = lpt;
+    t.lane = threadIdx.x % t.lpt;
+    const int per = NORM_NT / t.lpt;
+    t.item = (int64_t)blockIdx.x * per + threadIdx.x / t.lpt;
+    t.step = (int64_t)gridDim.x * per;  // a multiple of G: the group stays
+    t.c0 = (int)(t.item % a.G) * a.gs;
+    t.nv = a.gs / NormVec<T>::E;
+    // the same for all teams of the workgroup, which meet in team_sum
+    t.turns = (int)((a.rows * a.G - t.item + t.step - 1) / t.step);
+    if (WIDE) {
+        const int64_t first = (int64_t)blockIdx.x * per;
+        t.turns = first < a.rows * a.G ? (int)((a.rows * a.G - first + t.step - 1) / t.step) : 0;
+    }
+    return t;
+}
+
+// weight or bias of the lane's channels; `otherwise` where there is none
+template <typename T, int EPL>
+__device__ __forceinline__ void norm_params(const float* p, const NormTeam& t, float otherwise,
+                                            float (&o)[EPL]) {
+    constexpr int E = NormVec<T>::E;
+#pragma unroll
+    for (int i = 0; i < EPL / E; ++i) {
+        const int v = t.lane + i * t.lpt;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[i * E + e] = p && v < t.nv ? p[t.c0 + v * E + e] : otherwise;
+    }
+}
+
+template <typename T, int EPL>
+__device__ __forceinline__ void norm_load(const T* row, const NormTeam& t,
+                                          typename NormVec<T>::type (&o)[EPL / NormVec<T>::E]) {
+    typedef typename NormVec<T>::type vt;
+    constexpr int E = NormVec<T>::E;
+#pragma unroll
+    for (int i = 0; i < EPL / E; ++i) {
+        const int v = t.lane + i * t.lpt;
+        o[i] = v < t.nv ? *(const vt*)(row + v * E) : vt{};
+    }
+}
+
+// u, then n = (u - m) r, of the lane's channels (0 where it has none); returns r
+template <typename T, int EPL, int MODE, bool WIDE, bool TIGHT = false>
+__device__ __forceinline__ float norm_n(const NormArgs& a, const NormTeam& t,
+                                        const typename NormVec<T>::type (&x)[EPL / NormVec<T>::E],
+                                        const typename NormVec<T>::type (&z)[EPL / NormVec<T>::E],
+                                        float (&n)[EPL], float (*red)[NORM_NT / 64]) {
+    constexpr int E = NormVec<T>::E;
+    const float inv = 1.f / (float)a.gs;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        if (TIGHT && i % E == 0) __builtin_amdgcn_sched_barrier(0);
+        n[i] = (float)x[i / E][i % E];
+        if (MODE == SSD_NORM_BEFORE) {
+            const float zv = (float)z[i / E][i % E];
+            n[i] *= zv * sigm(zv);
+        }
+    }
+    if (a.center) {
+        float m[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) m[0] += n[i];
+        team_sum<1, WIDE>(m, t.lpt, red);
+        m[0] *= inv;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (t.lane + (i / E) * t.lpt < t.nv) n[i] -= m[0];
+    }
+    float q[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) q[0] += n[i] * n[i];
+    team_sum<1, WIDE>(q, t.lpt, red);
+    const float r = rsqrtf(q[0] * inv + a.eps);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) n[i] *= r;
+    return r;
+}
+
+template <typename T, int EPL, int MODE, bool WIDE>
+__global__ void __launch_bounds__(NORM_NT) k_norm_fwd(NormArgs a, int lpt) {
+    typedef typename NormVec<T>::type vt;
+    constexpr int E = NormVec<T>::E, V = EPL / E;
+    constexpr bool GATED = MODE >= SSD_NORM_BEFORE;
+    __shared__ float red[1][NORM_NT / 64];
+    const NormTeam t0 = norm_team<T, WIDE>(a, lpt);
+    float w[EPL], b[EPL];
+    norm_params<T, EPL>(a.w, t0, 0.f, w);
+    norm_params<T, EPL>(a.b, t0, 0.f, b);
+    NormTeam t = t0;
+    for (int k = 0; k < t0.turns; ++k) {
+        const int64_t it = t0.item + k * t0.step;
+        if (WIDE && it >= a.rows * a.G) t.nv = 0;  // nothing to load or store, only to meet
+        const int64_t row = WIDE && t.nv == 0 ? 0 : (uint32_t)it / (uint32_t)a.G;
+        vt x[V], z[V];
+        norm_load<T, EPL>((const T*)a.x + row * a.xs + t.c0, t, x);
+        if (GATED) norm_load<T, EPL>((const T*)a.z + row * a.zs + t.c0, t, z);
+        float n[EPL];
+        norm_n<T, EPL, MODE, WIDE>(a, t, x, z, n, red);
+        T* y = (T*)a.y + row * a.ys + t.c0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            vt o;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                float v = n[i * E + e] * w[i * E + e] + b[i * E + e];
+                if (MODE == SSD_NORM_SILU) v *= sigm(v);
+                if (MODE == SSD_NORM_AFTER) {
+                    const float zv = (float)z[i][e];
+                    v *= zv * sigm(zv);
+                }
+                o[e] = (T)v;
+            }
+            if (t.lane + i * t.lpt < t.nv) *(vt*)(y + (t.lane + i * t.lpt) * E) = o;
+        }
+    }
+}
+
+// Partial sums of dw and db: row p of part ([np][2][C]).  Where the workgroup's teams hold
+// whole sets of groups they are added in the workgroup first, team after team (`fold`).
+template <typename T, int EPL, int MODE, bool WIDE>
+__global__ void __launch_bounds__(NORM_NT, EPL == 8 ? 4 : 2) k_norm_bwd(NormArgs a, int lpt, int fold,
+                                                     float* __restrict__ part) {
+    typedef typename NormVec<T>::type vt;
+    constexpr int E = NormVec<T>::E, V = EPL / E;
+    constexpr bool GATED = MODE >= SSD_NORM_BEFORE;
+    __shared__ float red[2][NORM_NT / 64];
+    extern __shared__ __align__(16) float sums[];  // fold
+    const NormTeam t0 = norm_team<T, WIDE>(a, lpt);
+    const float inv = 1.f / (float)a.gs;
+    float w[EPL], b[MODE == SSD_NORM_SILU || MODE == SSD_NORM_AFTER ? EPL : 1];
+    norm_params<T, EPL>(a.w, t0, 0.f, w);
+    if constexpr (MODE == SSD_NORM_SILU || MODE == SSD_NORM_AFTER)
+        norm_params<T, EPL>(a.b, t0, 0.f, b);
+    float sw[EPL], sb[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) sw[i] = sb[i] = 0.f;
+    NormTeam t = t0;
+    for (int k = 0; k < t0.turns; ++k) {
+        const int64_t it = t0.item + k * t0.step;
+        if (WIDE && it >= a.rows * a.G) t.nv = 0;  // nothing to load or store, only to meet
+        const int64_t row = WIDE && t.nv == 0 ? 0 : (uint32_t)it / (uint32_t)a.G;
+        vt x[V], z[V], dy[V];
+        norm_load<T, EPL>((const T*)a.x + row * a.xs + t.c0, t, x);
+        if (GATED) norm_load<T, EPL>((const T*)a.z + row * a.zs + t.c0, t, z);
+        norm_load<T, EPL>((const T*)a.dy + row * a.ys + t.c0, t, dy);
+        float n[EPL], e[EPL];
+        const float r = norm_n<T, EPL, MODE, WIDE, true>(a, t, x, z, n, red);
+        float s[2] = {0.f, 0.f};  // sums of g n, g
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            // vector by vector: interleaved, their temporaries do not fit the registers
+            if (i % E == 0) __builtin_amdgcn_sched_barrier(0);
+            e[i] = (float)dy[i / E][i % E];
+            if (MODE == SSD_NORM_AFTER) {
+                const float zv = (float)z[i / E][i % E];
+                e[i] *= zv * sigm(zv);
+            }
+            if (MODE == SSD_NORM_SILU) {
+                const float lin = n[i] * w[i] + b[i];
+                const float sg = sigm(lin);
+                e[i] *= sg * (1.f + lin * (1.f - sg));
+            }
+            sw[i] += e[i] * n[i];
+            sb[i] += e[i];
+            e[i] *= w[i];
+            s[0] += e[i] * n[i];
+            s[1] += e[i];
+        }
+        team_sum<2, WIDE>(s, t.lpt, red);
+        s[0] *= inv;
+        s[1] = a.center ? s[1] * inv : 0.f;
+        // at 16 channels to a lane the gate is computed again from z, not held across the sums
+        if (EPL > 8)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                z[i] = forget(z[i]);
+                x[i] = forget(x[i]);
+                dy[i] = forget(dy[i]);
+            }
+        T* dx = (T*)a.dx + row * a.dxs + t.c0;
+        T* dz = (T*)a.dz + row * a.dzs + t.c0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int v = t.lane + i * t.lpt;
+            __builtin_amdgcn_sched_barrier(0);
+            vt ox, oz;
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const int c = i * E + j;
+                float du = r * (e[c] - s[1] - n[c] * s[0]);
+                if (GATED) {
+                    const float zv = (float)z[i][j], g = sigm(zv);
+                    const float ds = g * (1.f + zv * (1.f - g));
+                    if constexpr (MODE == SSD_NORM_BEFORE) {
+                        oz[j] = (T)(du * (float)x[i][j] * ds);
+                        du *= zv * g;
+                    } else if constexpr (MODE == SSD_NORM_AFTER) {
+                        oz[j] = (T)((float)dy[i][j] * (n[c] * w[c] + b[c]) * ds);
+                    }
+                }
+                ox[j] = (T)du;
+            }
+            if (v < t.nv) {
+                *(vt*)(dx + v * E) = ox;
+                if (GATED) *(vt*)(dz + v * E) = oz;
+            }
+        }
+    }
+    t = t0;
+    const int team = threadIdx.x / t.lpt, per = NORM_NT / t.lpt;
+    if (fold) {
+        // [dw, db][group][quad of a lane][lane] in LDS: each access a run of 16-byte vectors
+        const int gw = EPL * t.lpt, half = a.G * gw;
+        f32x4* mine = (f32x4*)(sums + team % a.G * gw) + t.lane;
+        for (int q = 0; q < per / a.G; ++q) {
+            if (team / a.G == q) {
+#pragma unroll
+                for (int i = 0; i < EPL; i += 4) {
+                    f32x4* p = mine + i / 4 * t.lpt;
+                    f32x4 vw = {sw[i], sw[i + 1], sw[i + 2], sw[i + 3]};
+                    f32x4 vb = {sb[i], sb[i + 1], sb[i + 2], sb[i + 3]};
+                    if (q) vw += p[0], vb += p[half / 4];
+                    p[0] = vw;
+                    p[half / 4] = vb;
+                }
+            }
+            __syncthreads();
+        }
+        float* p = part + (int64_t)blockIdx.x * 2 * a.C;
+        for (int i = threadIdx.x; i < 2 * a.C; i += NORM_NT) {
+            const int c = i % a.C, k = c % a.gs, v = k / E;  // vector v / lpt of lane v % lpt
+            const int el = v / t.lpt * E + k % E;
+            p[i] = sums[(i / a.C) * half + c / a.gs * gw + el / 4 * 4 * t.lpt + v % t.lpt * 4 + el % 4];
+        }
+    } else {
+        float* p = part + ((int64_t)blockIdx.x * per + team) / a.G * 2 * a.C + t.c0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int v = t.lane + (i / E) * t.lpt;
+            if (v < t.nv) {
+                p[v * E + i % E] = sw[i];
+                p[a.C + v * E + i % E] = sb[i];
+            }
+        }
+    }
+}
+
+// dw and db from the partial sums, 16 rows of them side by side, each in its order.
+__global__ void __launch_bounds__(1024) k_norm_reduce(const float* __restrict__ part, int np, int C,
+                                                      float* __restrict__ dw,
+                                                      float* __restrict__ db) {
+    __shared__ float red[16][64];
+    const int lane = threadIdx.x % 64, k = threadIdx.x / 64;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    float s = 0.f;
+    if (c < 2 * C)
+#pragma unroll 8
+        for (int p = k; p < np; p += 16) s += part[(int64_t)p * 2 * C + c];
+    red[k][lane] = s;
+    __syncthreads();
+    if (k == 0 && c < 2 * C) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += red[i][lane];
+        if (c < C) dw[c] = s;
+        else if (db) db[c - C] = s;
+    }
+}
+
+// How a problem is dealt out.
+struct NormPlan {
+    bool teams, wide, fold;
+    int epl, lpt, blocks, np;
+};
+
+static int64_t fold_lds(const NormArgs& a, const NormPlan& p) {
+    return 2ll * a.G * p.epl * p.lpt * 4;
+}
+
+static int gcd_of(int a, int b) {
+    while (b) {
+        const int r = a % b;
+        a = b;
+        b = r;
+    }
+    return a;
+}
+
+static NormPlan norm_plan(const NormArgs& a, int act, bool bwd, bool vectors) {
+    NormPlan p = {};
+    const int E = act == SSD_BF16 ? 8 : 4;
+    const int64_t items = a.rows * a.G;
+    // The fewest lanes that hold the group, at up to 32 channels to a lane in the forward
+    // and 16 in the backward, which has five values per channel (32 spill: 228 us for 16384
+    // rows of 2048 bf16 channels, NORM_BWD_16).
+    const int most = bwd ? 16 : 32;
+    p.teams = vectors && a.gs % E == 0 && a.gs <= most * NORM_NT;
+    p.epl = a.gs <= 8 * (bwd ? NORM_NT : 64) ? 8 : (a.gs <= 16 * 64 ? 16 : most);
+    p.lpt = 1;
+    while (p.lpt < NORM_NT && p.lpt * p.epl < a.gs) p.lpt *= 2;
+    p.wide = p.lpt > 64;
+    const int per = NORM_NT / p.lpt;          // teams per workgroup
+    const int unit = a.G / gcd_of(a.G, per);  // workgroups whose teams hold whole sets of groups
+    if (unit > 512) p.teams = false;          // thousands of groups, an odd number of them
+    if (!p.teams) {
+        const int64_t want = 1024 / a.G < 1 ? 1 : 1024 / a.G;
+        p.np = (int)(a.rows < want ? a.rows : want);
+        p.blocks = (int)(items < 65536 ? items : 65536);
+        return p;
+    }
+    // The backward runs one workgroup per CU twice over (its partial sums grow with them);
+    // the forward one for each two rows of a team, up to where the CUs are full many times.
+    const int64_t need = (items + per - 1) / per;
+    int64_t want = bwd ? 512 : (need + 1) / 2;
+    if (!bwd && want < 512) want = 512;
+    if (want > 16384) want = 16384;
+    if (want > need) want = need;
+    p.blocks = (int)((want + unit - 1) / unit) * unit;
+    p.fold = per % a.G == 0 && per / a.G > 1 && fold_lds(a, p) <= 60 * 1024;
+    p.np = p.fold ? p.blocks : (int)((int64_t)p.blocks * per / a.G);
+    return p;
+}
+
+size_t norm_bwd_ws(const NormArgs& a, int act) {
+    // either path may run, depending on the tensors' alignment
+    const int x = norm_plan(a, act, true, false).np, y = norm_plan(a, act, true, true).np;
+    return (size_t)(x > y ? x : y) * 2 * a.C * 4;
+}
+
+static bool norm_vectors(const NormArgs& a, int act, bool bwd) {
+    const int esz = act == SSD_BF16 ? 2 : 4;
+    auto ok = [&](const void* p, int64_t stride) {
+        return p == nullptr || (((uintptr_t)p & 15) == 0 && stride * esz % 16 == 0);
+    };
+    if (!ok(a.x, a.xs) || !ok(a.z, a.zs)) return false;
+    return bwd ? ok(a.dy, a.ys) && ok(a.dx, a.dxs) && ok(a.dz, a.dzs) : ok(a.y, a.ys);
+}
+
+template <typename T, int EPL, int MODE>
+static hipError_t norm_teams(const NormArgs& a, const NormPlan& p, float* part, hipStream_t s) {
+    const dim3 grid((unsigned)p.blocks), block(NORM_NT);
+    if (!part) {
+        if (p.wide) return launch(k_norm_fwd<T, EPL, MODE, true>, grid, block, s, a, p.lpt);
+        return launch(k_norm_fwd<T, EPL, MODE, false>, grid, block, s, a, p.lpt);
+    }
+    if constexpr (EPL <= 16) {
+        const int lds = p.fold ? (int)fold_lds(a, p) : 0;
+        if (p.wide)
+            return launch_lds(k_norm_bwd<T, EPL, MODE, true>, grid, block, lds, s, a, p.lpt,
+                              (int)p.fold, part);
+        return launch_lds(k_norm_bwd<T, EPL, MODE, false>, grid, block, lds, s, a, p.lpt,
+                          (int)p.fold, part);
+    }
+    return hipErrorInvalidValue;
+}
+
+template <typename T, int EPL>
+static hipError_t norm_mode(const NormArgs& a, const NormPlan& p, float* part, hipStream_t s) {
+    switch (a.mode) {
+        case SSD_NORM_NONE: return norm_teams<T, EPL, SSD_NORM_NONE>(a, p, part, s);
+        case SSD_NORM_SILU: return norm_teams<T, EPL, SSD_NORM_SILU>(a, p, part, s);
+        case SSD_NORM_BEFORE: return norm_teams<T, EPL, SSD_NORM_BEFORE>(a, p, part, s);
+        default: return norm_teams<T, EPL, SSD_NORM_AFTER>(a, p, part, s);
+    }
+}
+
+template <typename T>
+static hipError_t norm_t(const NormArgs& a, const NormPlan& p, float* part, hipStream_t s) {
+    if (!p.teams) {
+        if (!part) return launch(k_norm_fwd_any<T>, dim3((unsigned)p.blocks), dim3(256), s, a);
+        return launch(k_norm_bwd_any<T>, dim3((unsigned)p.np, (unsigned)a.G), dim3(256), s, a, part);
+    }
+    if (p.epl == 8) return norm_mode<T, 8>(a, p, part, s);
+    if (p.epl == 16) return norm_mode<T, 16>(a, p, part, s);
+    return norm_mode<T, 32>(a, p, nullptr, s);  // forward only
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, int act, hipStream_t s) {
-    const int64_t n = a.rows * a.G;
-    const dim3 grid((unsigned)(n < 65536 ? n : 65536));
-    if (act == SSD_BF16) return launch(k_norm_fwd_any<bf16>, grid, dim3(256), s, a);
-    return launch(k_norm_fwd_any<float>, grid, dim3(256), s, a);
+    const NormPlan p = norm_plan(a, act, false, norm_vectors(a, act, false));
+    return act == SSD_BF16 ? norm_t<bf16>(a, p, nullptr, s) : norm_t<float>(a, p, nullptr, s);
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, int act, float* part, hipStream_t s) {
-    const int nb = norm_row_blocks(a, act);
-    const dim3 grid((unsigned)nb, (unsigned)a.G);
-    if (act == SSD_BF16)
-        SSD_TRY(launch(k_norm_bwd_any<bf16>, grid, dim3(256), s, a, part));
-    else
-        SSD_TRY(launch(k_norm_bwd_any<float>, grid, dim3(256), s, a, part));
-    return launch(k_norm_reduce, dim3((unsigned)((a.C + 255) / 256)), dim3(256), s,
-                  (const float*)part, nb, a.C, a.dw, a.db);
+    const NormPlan p = norm_plan(a, act, true, norm_vectors(a, act, true));
+    SSD_TRY(act == SSD_BF16 ? norm_t<bf16>(a, p, part, s) : norm_t<float>(a, p, part, s));
+    return launch(k_norm_reduce, dim3((unsigned)((2 * (int64_t)a.C + 63) / 64)), dim3(1024), s,
+                  (const float*)part, p.np, a.C, a.dw, a.db);
 }
 
 }  // namespace ssd
