@@ -6,10 +6,8 @@
 // state that enters it:
 //   out_i = inter l^(i+1) M a_i + intra sum_{j<=i} l^(i-j) (b_j . a_i) c_j
 //   M     <- l^n M + s sum_j l^(n-1-j) c_j b_j^T
-// so the work is three matrix products per chunk, and M never leaves the registers: a
-// workgroup has 64 columns of M^T [BD][CD], each of its four waves 16 of them in float32
-// accumulators.  (Where CD is 128, two neighbouring workgroups form the same scores and read
-// the same a and b, the second time from L2.)
+// so the work is three matrix products per chunk, and M never leaves the registers: each of
+// the four waves of a workgroup keeps CD/4 columns of M^T [BD][CD] in float32 accumulators.
 //
 // A sequence is walked by as many workgroups as it has spans of `span` tokens (LaPlan).
 // Where a sequence has more than one, a first launch (OUT = false) leaves the state that
@@ -25,9 +23,10 @@
 //       are; c is read from LDS transposed (XT)
 //   M^T [bd][cd] = b^T (w c) : b is read transposed too, c's fragments are the ones above,
 //       weighted in registers
-// A bf16 k operand takes its 32 channels as 4g .. 4g+3 and 16+4g .. of lane group g (two
-// stacked tiles); rows of a and b stand in LDS with their channels in that order, so that
-// an operand is one 16-byte read.
+// A bf16 k operand holds 8 neighbouring channels of 32 to a lane, so the two accumulator
+// tiles that form one hold them 4 and 4: row 4g + r of tile t of M^T is channel
+// 32 (t / 2) + 8 g + 4 (t % 2) + r (la_channel).  That costs nothing, since the transposed
+// reads of b address their channels in quads of any order.
 //
 // Precision.  Scores and the entering state are rounded to bf16 once as operands.  The
 // weighted c are not: a state is a float32 result, and one rounding would leave 2^-9 of it.
@@ -50,14 +49,18 @@ template <> struct LaCfg<float> {
     static constexpr int TPK = 1;
 };
 
-// The spans of all sequences, numbered so that no scan over the lengths is needed:
-// sequence s owns the numbers lo_s / span + s .. (as many as it has spans, and at least
-// one), of which the ones behind its last span are idle.
+// The spans of all sequences, numbered so that no scan over the lengths is needed: row s
+// owns the numbers s per_row ..; packed sequence s owns lo_s / span + s .. (as many as it has
+// spans, and at least one), of which the ones behind its last span are idle.
 struct LaPlan {
     int span;       // tokens per span, a multiple of the chunk
+    int per_row;    // spans of a row (no cu_seqlens)
     int64_t slots;  // numbers handed out
     bool split;     // some sequence may have more than one span
 };
+__device__ __forceinline__ int64_t la_first_slot(const LaWalk& w, const LaPlan& p, int s) {
+    return w.cu ? seq_range(w, s).lo / p.span + s : (int64_t)s * p.per_row;
+}
 
 struct LaSpan {
     int s, j;         // sequence, span of it; s < 0: idle
@@ -68,13 +71,14 @@ struct LaSpan {
 
 __device__ __forceinline__ LaSpan la_span(const LaWalk& w, const LaPlan& p, int64_t slot) {
     int a = 0, b = w.nseq - 1;  // the last sequence whose numbers start at or below slot
+    if (!w.cu) a = b = (int)(slot / p.per_row);
     while (a < b) {
         const int m = (a + b + 1) / 2;
-        if (seq_range(w, m).lo / p.span + m <= slot) a = m;
+        if (la_first_slot(w, p, m) <= slot) a = m;
         else b = m - 1;
     }
     const SeqRange r = seq_range(w, a);
-    const int64_t j = slot - (r.lo / p.span + a), len = r.hi - r.lo;
+    const int64_t j = slot - la_first_slot(w, p, a), len = r.hi - r.lo;
     LaSpan s;
     s.s = j < 0 || (j > 0 && j * p.span >= len) ? -1 : a;
     s.j = (int)j;
@@ -86,6 +90,22 @@ __device__ __forceinline__ LaSpan la_span(const LaWalk& w, const LaPlan& p, int6
     return s;
 }
 
+// Whether one of a vector's values is not finite.
+__device__ __forceinline__ unsigned la_ones(unsigned u) {
+    // a half's exponent of ones carries into its top bit
+    return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+typedef unsigned la_u4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ bool la_wild(bf16x8 v) {
+    const la_u4 u = __builtin_bit_cast(la_u4, v);
+    return (la_ones(u[0]) | la_ones(u[1]) | la_ones(u[2]) | la_ones(u[3])) != 0;
+}
+__device__ __forceinline__ bool la_wild(f32x4 v) {
+    bool m = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = m || !(fabsf(v[i]) < INFINITY);
+    return m;
+}
 // Rows of one operand on their way into LDS: 16-byte vectors of D channels per token.
 // They come through bounded buffer loads, which give zeros for rows without a token and
 // need no branch or select: the n tokens of a last chunk take its last rows, so that the
@@ -115,24 +135,22 @@ struct LaRows {
 #pragma unroll
         for (int i = 0; i < NP; ++i) *(vt*)(lds + (r0 + i * RPP) * PITCH + c) = v[i];
     }
-    // the same with the channels in k operand order
-    __device__ __forceinline__ void store_k(T* lds) const {
-        if constexpr (sizeof(T) == 4) {
-            store(lds);
-        } else {
-            const int r0 = threadIdx.x / VPR, q = threadIdx.x % VPR, m = q % 4;
-            T* p = lds + r0 * PITCH + 32 * (q / 4) + 16 * (m & 1) + 4 * (m >> 1);
+    // whether a value is not finite
+    __device__ __forceinline__ bool wild() const {
+        bool m = false;
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                *(bf16x4*)(p + i * RPP * PITCH) = __builtin_shufflevector(v[i], v[i], 0, 1, 2, 3);
-                *(bf16x4*)(p + i * RPP * PITCH + 8) = __builtin_shufflevector(v[i], v[i], 4, 5, 6, 7);
-            }
-        }
+        for (int i = 0; i < NP; ++i) m = m || la_wild(v[i]);
+        return m;
     }
 };
 
-// b^T as the row operand of M^T: rows are channels 16 t .., k the tokens from jb, b's rows
-// being stored with channels in k operand order.
+// Channel of row 4 lg of tile t of M^T.
+template <typename T>
+__device__ __forceinline__ int la_channel(int t, int lg) {
+    return sizeof(T) == 4 ? 16 * t + 4 * lg : 32 * (t / 2) + 8 * lg + 4 * (t % 2);
+}
+
+// b^T as the row operand of tile t of M^T, k the tokens from jb.
 template <typename T>
 __device__ __forceinline__ typename Mma<T>::Frag la_bt(const T* b, int pitch, int jb, int t,
                                                        int lane) {
@@ -170,43 +188,60 @@ __device__ __forceinline__ float la_pow(double l2, int e) {
 
 enum LaOut { LA_STATE = 0, LA_ACT = 1, LA_F32 = 2 };  // what a walk leaves behind
 
-template <typename T, int BD, int OUT>
+template <typename T, int BD, int CD, int OUT>
 constexpr int la_lds_bytes() {
     constexpr int Q = LaCfg<T>::Q, V = 16 / (int)sizeof(T), NT = Q / 16;
-    return Q * (BD + V) * (int)sizeof(T) * (OUT ? 2 : 1) + Q * (64 + V) * (int)sizeof(T) +
-           (OUT ? NT * (NT / LaCfg<T>::TPK) * 1024 : 0);
+    return Q * (BD + V) * (int)sizeof(T) * (OUT ? 2 : 1) + Q * (CD + V) * (int)sizeof(T) +
+           (OUT ? NT * (NT / LaCfg<T>::TPK) * 1024 + 16 + CD * 4 : 0);
 }
 
-// Workgroup of four waves per (span, head, 64 columns).  SPLITS: bf16 terms per weighted c
-// (1 for float32).  `ws`: the spans' states, [slot][H][CD / 64][wave][tile][lane] f32x4.
-template <typename T, int BD, bool REV, int OUT, int SPLITS>
-__global__ void __launch_bounds__(256, BD == 64 ? 3 : 2) k_la_walk(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
+// Waves per SIMD that a walk's registers allow.
+template <int BD, int CD, int OUT>
+constexpr int la_waves() {
+    return OUT && BD + CD > 128 ? 2 : 3;
+}
+
+// Workgroup of four waves per (span, head).  SPLITS: bf16 terms per weighted c (1 for
+// float32).  `ws`: the spans' states, [slot][H][wave][tile][lane] f32x4.
+//
+// A c_j that is not finite times a masked score's 0 would be NaN in the outputs before j.  A
+// chunk that has one puts 0 in its place, and NaN into the state and, from j on, the
+// outputs of its channel.  Both happen where few registers are live.
+template <typename T, int BD, int CD, bool REV, int OUT, int SPLITS>
+__global__ void __launch_bounds__(256, (la_waves<BD, CD, OUT>()))
+k_la_walk(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
     typedef Mma<T> M;
     typedef typename M::Frag Frag;
     constexpr int Q = LaCfg<T>::Q, TPK = LaCfg<T>::TPK, NT = Q / 16, NK = NT / TPK;
     constexpr int SL = M::SL, KS = M::KS, KB = BD / KS;
-    constexpr int BT = BD / 16;  // tiles of M^T of one wave
-    constexpr int AP = LaRows<T, BD, REV>::PITCH, CP = LaRows<T, 64, REV>::PITCH;
-    __shared__ __align__(16) unsigned char lds[la_lds_bytes<T, BD, OUT>()];
+    constexpr int BT = BD / 16, CW = CD / 4, CT = CW / 16;  // tiles of M^T of one wave
+    constexpr int AP = LaRows<T, BD, REV>::PITCH, CP = LaRows<T, CD, REV>::PITCH;
+    __shared__ __align__(16) unsigned char lds[la_lds_bytes<T, BD, CD, OUT>()];
     T* sb = (T*)lds;
     T* sc = sb + Q * AP;
     T* sa = sc + Q * CP;
     Frag* sp = (Frag*)(sa + Q * AP);  // scores, [row tile][k block][lane]
+    int* wild = (int*)(sp + NT * NK * 64);  // a c of the chunk is not finite
+    int* wild_row = wild + 4;               // the first such row of each channel, or Q
+    if (OUT && threadIdx.x == 0) *wild = 0;
 
-    // consecutive items (the column halves and heads that share rows) go to one XCD
-    const int64_t nblk = gridDim.x;
-    int64_t item = nblk % 8 == 0 ? (blockIdx.x % 8) * (nblk / 8) + blockIdx.x / 8 : blockIdx.x;
-    const int CD = w.cd, nct = CD / 64;
-    const int ct = (int)(item % nct);
-    item /= nct;
-    const int h = (int)(item % w.H);
-    const int64_t slot = item / w.H;
+    // The hardware deals workgroups out over the 8 XCDs in turn.  The heads that share keys
+    // and values go to one XCD, whose L2 then holds them; such groups, and with them the
+    // idle numbers, are spread over all (in contiguous ranges to an XCD, idle ones leave some
+    // XCDs with more spans than they have room for at once: 119 us instead of 8x us for the
+    // walk of 2 x 8192 tokens, 32 heads of 128 x 64).
+    const int share = w.share;
+    const int64_t unit = blockIdx.x / 8 / share * 8 + blockIdx.x % 8;
+    const int groups = w.H / share;
+    const int64_t slot = unit / groups;
+    if (slot >= plan.slots) return;
+    const int h = (int)(unit % groups) * share + (int)(blockIdx.x / 8 % share);
     const LaSpan sp_ = la_span(w, plan, slot);
     if (sp_.s < 0 || (!OUT && sp_.last)) return;
     const int wave = wave_id(), lane = threadIdx.x % 64, lr = lane % 16, lg = lane / 16;
     const T* pa = (const T*)w.a + (int64_t)(h / w.a_div) * BD;
     const T* pb = (const T*)w.b + (int64_t)(h / w.b_div) * BD;
-    const T* pc = (const T*)w.c + (int64_t)(h / w.c_div) * CD + ct * 64;
+    const T* pc = (const T*)w.c + (int64_t)(h / w.c_div) * CD;
     const int ats = (int)w.a_ts, bts = (int)w.b_ts, cts = (int)w.c_ts;
     const int nch = (sp_.n + Q - 1) / Q;
 
@@ -217,7 +252,7 @@ __global__ void __launch_bounds__(256, BD == 64 ? 3 : 2) k_la_walk(LaWalk w, LaP
     };
     auto tokens_of = [&](int k) { return sp_.n - k * Q < Q ? sp_.n - k * Q : Q; };
     LaRows<T, BD, REV> ra, rb;
-    LaRows<T, 64, REV> rc;
+    LaRows<T, CD, REV> rc;
     auto load = [&](int k) {
         const int n = tokens_of(k);
         const int64_t t0 = first_token(k, n);
@@ -227,28 +262,39 @@ __global__ void __launch_bounds__(256, BD == 64 ? 3 : 2) k_la_walk(LaWalk w, LaP
     };
     if (nch > 0) load(0);
 
-    // the state that enters the span; this lane's elements of tile t are channels
-    // 16 t + 4 lg .. of b and channel `col` of c
-    f32x4 St[BT];
-    const int col = ct * 64 + wave * 16 + lr;
+    // the state that enters the span; this lane's elements of tile (t, u) are the four
+    // channels of b from la_channel and channel 16 u + `col` of c
+    f32x4 St[BT][CT];
+    const int col = wave * CW + lr;
     const bool given = sp_.j == 0;
-    f32x4* mine = ws + (((slot * w.H + h) * nct + ct) * 4 + wave) * (BT * 64) + lane;
-    const int64_t state_at = ((int64_t)sp_.s * w.H + h) * ((int64_t)BD * CD) +
-                             (w.trans ? (int64_t)4 * lg * CD + col : (int64_t)col * BD + 4 * lg);
+    f32x4* mine = ws + ((slot * w.H + h) * 4 + wave) * (BT * CT * 64) + lane;
+    const int64_t state_at = ((int64_t)sp_.s * w.H + h) * (BD * CD);
+    auto at = [&](int t, int u) { return (col + 16 * u) * BD + la_channel<T>(t, lg); };
+    auto at_trans = [&](int t, int u, int r) {
+        return (la_channel<T>(t, lg) + r) * CD + col + 16 * u;
+    };
     if (OUT && !given) {
 #pragma unroll
-        for (int t = 0; t < BT; ++t) St[t] = mine[t * 64];
+        for (int t = 0; t < BT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) St[t][u] = mine[(t * CT + u) * 64];
     } else if (given && w.init && !w.trans) {
 #pragma unroll
-        for (int t = 0; t < BT; ++t) St[t] = *(const f32x4*)(w.init + state_at + 16 * t);
+        for (int t = 0; t < BT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) St[t][u] = *(const f32x4*)(w.init + state_at + at(t, u));
     } else if (given && w.init) {
 #pragma unroll
         for (int t = 0; t < BT; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) St[t][r] = w.init[state_at + (int64_t)(16 * t + r) * CD];
+            for (int u = 0; u < CT; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) St[t][u][r] = w.init[state_at + at_trans(t, u, r)];
     } else {
 #pragma unroll
-        for (int t = 0; t < BT; ++t) St[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < BT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) St[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
     const float ld = w.log_decay[h];
@@ -265,13 +311,16 @@ __global__ void __launch_bounds__(256, BD == 64 ? 3 : 2) k_la_walk(LaWalk w, LaP
             lw[r] = w.intra * la_pow(l2, 16 + d);
         }
     }
-    float wk[NK][SL];  // s l^(Q-1-j) of the lane's k slots
+    // s l^(Q-1-j) of the lane's k slots, j = KS k + 16 (s / 4) + 4 lg + s % 4: a factor of
+    // the lane's and one that all lanes share, held as a scalar
+    const float wl = la_pow(l2, 12 - 4 * lg);
+    float wk[NK][SL];
 #pragma unroll
     for (int k = 0; k < NK; ++k)
 #pragma unroll
         for (int s = 0; s < SL; ++s)
-            wk[k][s] = w.state_scale *
-                       la_pow(l2, Q - 1 - (KS * k + 16 * (s / 4) + 4 * lg + s % 4));
+            wk[k][s] = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(
+                w.state_scale * la_pow(l2, Q - 13 - (KS * k + 16 * (s / 4) + s % 4)))));
     // The given state of a REV walk is not decayed before its first use.
     const bool late = REV && given;
     // l^n, compounded from chunk to chunk: the exact power, rounded once
@@ -288,12 +337,18 @@ __global__ void __launch_bounds__(256, BD == 64 ? 3 : 2) k_la_walk(LaWalk w, LaP
     for (int k = 0; k < nch; ++k) {
         const int n = tokens_of(k);
         __syncthreads();  // the last chunk's reads are done
-        rb.store_k(sb);
+        rb.store(sb);
         rc.store(sc);
-        if constexpr (OUT) ra.store_k(sa);
+        if constexpr (OUT) {
+            ra.store(sa);
+            if (rc.wild()) *wild = 1;
+        }
         __syncthreads();
-        // the last chunk's prefetch repeats it: no branch, so no full waits at a join
-        load(k + 1 < nch ? k + 1 : k);
+        bool tame = false;
+        // The next chunk's rows are fetched once the scores and M a_i are done, whose
+        // registers theirs would not fit beside; the last chunk's fetch repeats it (no branch,
+        // so no full waits at a join).
+        if constexpr (!OUT) load(k + 1 < nch ? k + 1 : k);
         const float keep = k + 1 == nch ? llast : (k == 0 ? lfirst : lq);
         if (OUT && n != Q) {  // the last chunk's tokens begin at row Q - n
             int i0 = lr - (Q - n) + (late && k == 0 ? 0 : 1);
@@ -303,7 +358,7 @@ __global__ void __launch_bounds__(256, BD == 64 ? 3 : 2) k_la_walk(LaWalk w, LaP
                 row[t] = w.inter * la_pow(l2, 16 * t + i0 > 0 ? 16 * t + i0 : 0);
         }
 
-        f32x4 o[NT];
+        f32x4 o[NT][CT];
         if constexpr (OUT) {
             // scores of row tile `wave`: k blocks up to the diagonal
             if (wave < NT) {
@@ -339,89 +394,95 @@ __global__ void __launch_bounds__(256, BD == 64 ? 3 : 2) k_la_walk(LaWalk w, LaP
                     sp[(wave * NK + kb) * 64 + lane] = la_frag<T>(tl);
                 }
             }
+            if (*wild) {  // for the whole workgroup
+                tame = true;
+                if (threadIdx.x < CD) {
+                    int first = Q;
+#pragma unroll 1
+                    for (int j = Q - 1; j >= 0; --j)
+                        if (!(fabsf((float)sc[j * CP + threadIdx.x]) < INFINITY)) {
+                            sc[j * CP + threadIdx.x] = (T)0.f;
+                            first = j;
+                        }
+                    wild_row[threadIdx.x] = first;
+                }
+                __syncthreads();  // before bar 2 every wave has read the flag
+                if (threadIdx.x == 0) *wild = 0;
+            }
             // l^(i+1) M a_i
 #pragma unroll
-            for (int t = 0; t < NT; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int u = 0; u < CT; ++u) o[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < KB; ++q) {
-                const Frag sf = la_frag<T>(&St[q * TPK]);
+                Frag sf[CT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    o[t] = M::mma(sf, M::load(sa + (16 * t + lr) * AP + KS * q + SL * lg), o[t]);
-            }
+                for (int u = 0; u < CT; ++u) {
+                    f32x4 tl[TPK];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) o[t] *= row[t];
-            __syncthreads();  // the scores are there
-        }
-
-        Frag cf[NK];
+                    for (int e = 0; e < TPK; ++e) tl[e] = St[q * TPK + e][u];
+                    sf[u] = la_frag<T>(tl);
+                }
 #pragma unroll
-        for (int kb = 0; kb < NK; ++kb) cf[kb] = XT<T>::load(sc, CP, KS * kb, wave * 16, lane);
-        // w_j c_j, and whether one of this wave's c is not finite
-        float x[NK][SL], all = 0.f;
+                for (int t = 0; t < NT; ++t) {
+                    const Frag a = M::load(sa + (16 * t + lr) * AP + KS * q + SL * lg);
 #pragma unroll
-        for (int kb = 0; kb < NK; ++kb)
-#pragma unroll
-            for (int s = 0; s < SL; ++s) {
-                x[kb][s] = (float)cf[kb][s] * wk[kb][s];
-                all += x[kb][s];
-            }
-        if constexpr (OUT) {
-            // A c_j that is not finite times a masked score's 0 would be NaN in the outputs
-            // before j too.  It is taken out of the product, and the outputs of its channel
-            // from j on are set.
-            const bool wild = __ballot(!(fabsf(all) < INFINITY)) != 0;
-            int from[4];
-            if (wild) {
-                int j0 = Q;
-                int g4 = 4 * lg;
-                asm volatile("" : "+v"(g4));
-#pragma unroll
-                for (int kb = NK - 1; kb >= 0; --kb)
-#pragma unroll
-                    for (int s = SL - 1; s >= 0; --s)
-                        if (!(fabsf((float)cf[kb][s]) < INFINITY)) {
-                            j0 = KS * kb + 16 * (s / 4) + s % 4 + g4;
-                            cf[kb][s] = (T)0.f;
-                        }
-                j0 = min(j0, __shfl_xor(j0, 16, 64));
-                j0 = min(j0, __shfl_xor(j0, 32, 64));
-#pragma unroll
-                for (int r = 0; r < 4; ++r) from[r] = __shfl(j0, 4 * lg + r, 64);
+                    for (int u = 0; u < CT; ++u) o[t][u] = M::mma(sf[u], a, o[t][u]);
+                }
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int kb = 0; kb <= t / TPK; ++kb)
-                    o[t] = M::mma(cf[kb], sp[(t * NK + kb) * 64 + lane], o[t]);
-            if (wild) {
+                for (int u = 0; u < CT; ++u) o[t][u] *= row[t];
+            __builtin_amdgcn_sched_barrier(0);
+            load(k + 1 < nch ? k + 1 : k);
+            __syncthreads();  // the scores are there
+        }
+
+        Frag cf[NK][CT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+        for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (16 * t + lr >= from[r]) o[t][r] = NAN;
-            }
+            for (int u = 0; u < CT; ++u)
+                cf[kb][u] = XT<T>::load(sc, CP, KS * kb, wave * CW + 16 * u, lane);
+        if constexpr (OUT) {
+#pragma unroll
+            for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+                for (int t = kb * TPK; t < NT; ++t) {
+                    const Frag p = sp[(t * NK + kb) * 64 + lane];
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) o[t][u] = M::mma(cf[kb][u], p, o[t][u]);
+                }
         }
 
         // M <- l^n M + b^T (w c)
 #pragma unroll
-        for (int t = 0; t < BT; ++t) St[t] *= keep;
+        for (int t = 0; t < BT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) St[t][u] *= keep;
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
-            Frag wc[SPLITS];
+            Frag wc[SPLITS][CT];
 #pragma unroll
-            for (int s = 0; s < SL; ++s) {
+            for (int u = 0; u < CT; ++u)
 #pragma unroll
-                for (int p = 0; p < SPLITS; ++p) {
-                    wc[p][s] = (T)x[kb][s];
-                    x[kb][s] -= (float)wc[p][s];
+                for (int s = 0; s < SL; ++s) {
+                    float x = (float)cf[kb][u][s] * wl * wk[kb][s];
+#pragma unroll
+                    for (int p = 0; p < SPLITS; ++p) {
+                        wc[p][u][s] = (T)x;
+                        x -= (float)wc[p][u][s];
+                    }
                 }
-            }
 #pragma unroll
             for (int t = 0; t < BT; ++t) {
                 const Frag bt = la_bt<T>(sb, AP, KS * kb, t, lane);
 #pragma unroll
-                for (int p = SPLITS - 1; p >= 0; --p) St[t] = M::mma(bt, wc[p], St[t]);
+                for (int p = SPLITS - 1; p >= 0; --p)
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) St[t][u] = M::mma(bt, wc[p][u], St[t][u]);
             }
         }
 
@@ -430,40 +491,66 @@ __global__ void __launch_bounds__(256, BD == 64 ? 3 : 2) k_la_walk(LaWalk w, LaP
             // beyond the buffer's bound
             typedef typename std::conditional<OUT == LA_F32, float, T>::type OT;
             typedef typename Vec4<OT>::type ov;
-            const __amdgpu_buffer_rsrc_t r =
-                buf_rsrc((OT*)w.out + first_token(k, n) * w.out_ts + (int64_t)h * CD + ct * 64,
-                         n * out_bytes);
+            const __amdgpu_buffer_rsrc_t r = buf_rsrc(
+                (OT*)w.out + first_token(k, n) * w.out_ts + (int64_t)h * CD, n * out_bytes);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int i = 16 * t + lr;
-                ov v;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[c] = (OT)o[t][c];
-                buf_store(v, r, (REV ? Q - 1 - i : i - (Q - n)) * out_bytes +
-                                    (wave * 16 + 4 * lg) * (int)sizeof(OT));
+                for (int u = 0; u < CT; ++u) {
+                    ov v;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[c] = (OT)o[t][u][c];
+                    buf_store(v, r, (REV ? Q - 1 - i : i - (Q - n)) * out_bytes +
+                                        (wave * CW + 16 * u + 4 * lg) * (int)sizeof(OT));
+                }
             }
         }
         if (late && k == 0) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) row[t] *= l1;
         }
+        if constexpr (OUT)
+            if (tame) {
+#pragma unroll
+                for (int u = 0; u < CT; ++u)
+                    if (wild_row[col + 16 * u] < Q)
+#pragma unroll
+                        for (int t = 0; t < BT; ++t) St[t][u] = f32x4{NAN, NAN, NAN, NAN};
+                // over the rows that this wave has just stored
+                typedef typename std::conditional<OUT == LA_F32, float, T>::type OT;
+                __threadfence();
+#pragma unroll 1
+                for (int i = Q - n + lane; i < Q; i += 64) {
+                    const int64_t tok = first_token(k, n) + (REV ? Q - 1 - i : i - (Q - n));
+                    OT* p = (OT*)w.out + tok * w.out_ts + (int64_t)h * CD;
+#pragma unroll 1
+                    for (int c = wave * CW; c < wave * CW + CW; ++c)
+                        if (i >= wild_row[c]) p[c] = (OT)NAN;
+                }
+            }
     }
 
     if constexpr (!OUT) {
 #pragma unroll
-        for (int t = 0; t < BT; ++t) mine[t * 64] = St[t];
+        for (int t = 0; t < BT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) mine[(t * CT + u) * 64] = St[t][u];
     } else if (w.fin && sp_.last) {
-        const float keep = REV && sp_.n > 0 ? (float)exp((double)ld) : 1.f;
+        const float keep = REV && sp_.n > 0 ? power(1) : 1.f;
 #pragma unroll
-        for (int t = 0; t < BT; ++t) {
-            const f32x4 v = St[t] * keep;
-            if (w.trans) {
+        for (int t = 0; t < BT; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) w.fin[state_at + (int64_t)(16 * t + r) * CD] = v[r];
-            } else {
-                *(f32x4*)(w.fin + state_at + 16 * t) = v;
+            for (int u = 0; u < CT; ++u) {
+                const f32x4 v = St[t][u] * keep;
+                float* p = w.fin + state_at;
+                if (w.trans) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) p[at_trans(t, u, r)] = v[r];
+                } else {
+                    *(f32x4*)(p + at(t, u)) = v;
+                }
             }
-        }
     }
 }
 

@@ -16,7 +16,7 @@ __global__ void __launch_bounds__(256) k_la_spans(LaWalk w, LaPlan plan, int qua
     if (n < 2) return;
     const float keep = (float)exp((double)plan.span * (double)w.log_decay[h]);
     const int64_t step = (int64_t)w.H * quads;
-    f32x4* p = ws + (r.lo / plan.span + s) * step + (int64_t)h * quads + q;
+    f32x4* p = ws + la_first_slot(w, plan, s) * step + (int64_t)h * quads + q;
     f32x4 m = *p;
     for (int64_t j = 1; j < n; ++j) {
         p += step;
@@ -49,10 +49,11 @@ __global__ void __launch_bounds__(256) k_la_group_sum(LaWalk w, const float* __r
 constexpr int LA_BLOCKS = 512, LA_MIN_SPAN = 256;
 
 static LaPlan la_plan(const LaWalk& w) {
-    const int64_t per = (w.tokens * w.H * (w.cd / 64) + LA_BLOCKS - 1) / LA_BLOCKS;
+    const int64_t per = (w.tokens * w.H + LA_BLOCKS - 1) / LA_BLOCKS;
     LaPlan p;
     p.span = (int)((per > LA_MIN_SPAN ? per + 63 : LA_MIN_SPAN) / 64 * 64);
-    p.slots = w.tokens / p.span + w.nseq;
+    p.per_row = (int)((w.seqlen + p.span - 1) / p.span);
+    p.slots = w.cu ? w.tokens / p.span + w.nseq : (int64_t)w.nseq * p.per_row;
     p.split = (w.cu ? w.tokens : w.seqlen) > p.span;
     return p;
 }
@@ -62,33 +63,40 @@ size_t la_walk_ws(const LaWalk& w, int) {
     return p.split ? (size_t)p.slots * w.H * w.bd * w.cd * 4 : 0;
 }
 
-template <typename T, int BD, bool REV>
+template <typename T, int BD, int CD, bool REV>
 static hipError_t walk_shape(const LaWalk& w, f32x4* ws, hipStream_t s) {
     constexpr int FINE = sizeof(T) == 2 ? 3 : 1, FAST = sizeof(T) == 2 ? 2 : 1;
     const LaPlan p = la_plan(w);
-    const dim3 grid((unsigned)(p.slots * w.H * (w.cd / 64))), block(256);
+    const int64_t units = p.slots * (w.H / w.share);
+    const dim3 grid((unsigned)((units + 7) / 8 * 8 * w.share)), block(256);
     if (p.split) {
-        SSD_TRY(launch(k_la_walk<T, BD, REV, LA_STATE, FINE>, grid, block, s, w, p, ws));
-        const int quads = BD * w.cd / 4;
+        SSD_TRY(launch(k_la_walk<T, BD, CD, REV, LA_STATE, FINE>, grid, block, s, w, p, ws));
+        constexpr int quads = BD * CD / 4;
         SSD_TRY(launch(k_la_spans, dim3((unsigned)((int64_t)w.nseq * w.H * (quads / 256))),
                        dim3(256), s, w, p, quads, ws));
     }
     if constexpr (REV)
         if (w.out_f32) {
-            if (w.fin) return launch(k_la_walk<T, BD, REV, LA_F32, FINE>, grid, block, s, w, p, ws);
-            return launch(k_la_walk<T, BD, REV, LA_F32, FAST>, grid, block, s, w, p, ws);
+            if (w.fin)
+                return launch(k_la_walk<T, BD, CD, REV, LA_F32, FINE>, grid, block, s, w, p, ws);
+            return launch(k_la_walk<T, BD, CD, REV, LA_F32, FAST>, grid, block, s, w, p, ws);
         }
-    if (w.fin) return launch(k_la_walk<T, BD, REV, LA_ACT, FINE>, grid, block, s, w, p, ws);
-    return launch(k_la_walk<T, BD, REV, LA_ACT, FAST>, grid, block, s, w, p, ws);
+    if (w.fin) return launch(k_la_walk<T, BD, CD, REV, LA_ACT, FINE>, grid, block, s, w, p, ws);
+    return launch(k_la_walk<T, BD, CD, REV, LA_ACT, FAST>, grid, block, s, w, p, ws);
+}
+
+template <typename T, bool REV>
+static hipError_t walk_dims(const LaWalk& w, f32x4* ws, hipStream_t s) {
+    if (w.bd == 64) return w.cd == 64 ? walk_shape<T, 64, 64, REV>(w, ws, s)
+                                      : walk_shape<T, 64, 128, REV>(w, ws, s);
+    return w.cd == 64 ? walk_shape<T, 128, 64, REV>(w, ws, s)
+                      : walk_shape<T, 128, 128, REV>(w, ws, s);
 }
 
 template <typename T>
 static hipError_t walk_t(const LaWalk& w, void* ws, hipStream_t s) {
-    if (w.bd == 64)
-        return w.reverse ? walk_shape<T, 64, true>(w, (f32x4*)ws, s)
-                         : walk_shape<T, 64, false>(w, (f32x4*)ws, s);
-    return w.reverse ? walk_shape<T, 128, true>(w, (f32x4*)ws, s)
-                     : walk_shape<T, 128, false>(w, (f32x4*)ws, s);
+    return w.reverse ? walk_dims<T, true>(w, (f32x4*)ws, s)
+                     : walk_dims<T, false>(w, (f32x4*)ws, s);
 }
 
 bool la_supported(int keydim, int valdim, int act) {

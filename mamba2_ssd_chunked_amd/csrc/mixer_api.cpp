@@ -63,6 +63,7 @@ LaWalk base_walk(const ssd_linattn* p, int32_t nseq, const float* log_decay, con
     w.seqlen = p->seqlen;
     w.tokens = p->batch * p->seqlen;
     w.H = p->nheads;
+    w.share = p->nheads / p->nkvheads;
     w.a_div = w.b_div = w.c_div = 1;
     return w;
 }
@@ -145,12 +146,12 @@ size_t linattn_ws(const ssd_linattn* p, const LaStrides& st, int32_t nseq, int32
     return part_bytes(p) + n;
 }
 
-// Every launch of the walks fits: up to two workgroups per (span, head), spans of at least
-// 256 tokens, and up to 16 per (sequence, head) to compose span states.
+// Every launch of the walks fits: a workgroup per (span, head), spans of at least 256 tokens
+// (rounded up to 8 spans), and up to 16 per (sequence, head) to compose span states.
 int check_walk_grid(const ssd_linattn* p, int32_t nseq) {
     typedef unsigned __int128 u128;
     const u128 spans = (u128)(p->batch * p->seqlen) / 256 + nseq;
-    const u128 blocks = (2 * spans > (u128)nseq * 16 ? 2 * spans : (u128)nseq * 16) * p->nheads;
+    const u128 blocks = (spans + 8 > (u128)nseq * 16 ? spans + 8 : (u128)nseq * 16) * p->nheads;
     return blocks <= (u128)MAX_BLOCKS ? SSD_OK : SSD_ERR_SHAPE;
 }
 

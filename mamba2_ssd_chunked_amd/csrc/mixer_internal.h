@@ -45,7 +45,7 @@ struct LaWalk {
     bool reverse;                    // from the last token; the given state then meets the
                                      // first visited token undecayed, and `fin` is decayed
     float intra, inter, state_scale; // factors of c_j (b_j . a_i), of M a_i, of c b^T into M
-    int H;
+    int H, share;                    // heads; neighbouring heads that share keys and values
 };
 
 // Sequence s as token range [lo, hi) over all rows; offsets outside the tokens are cut
