@@ -55,7 +55,7 @@ typedef struct {
     int64_t q_stride, k_stride, v_stride, o_stride;
     int64_t dq_stride, dk_stride, dv_stride;
 } ssd_linattn;
-/* Size limits (SSD_ERR_SHAPE beyond them): batch * seqlen <= 2^31 - 1 tokens,
+/* Size limits (SSD_ERR_SHAPE beyond them): batch * seqlen <= 2^31 - 128 tokens,
  * nheads <= 65535, sequences <= 2^24, token strides below 2^23 elements, and every
  * launch grid within the hardware's limits. */
 

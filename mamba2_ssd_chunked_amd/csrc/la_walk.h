@@ -195,28 +195,34 @@ constexpr int la_lds_bytes() {
            (OUT ? NT * (NT / LaCfg<T>::TPK) * 1024 + 16 + CD * 4 : 0);
 }
 
-// Waves per SIMD that a walk's registers allow.
-template <int BD, int CD, int OUT>
-constexpr int la_waves() {
-    return OUT && BD + CD > 128 ? 2 : 3;
+// Two accumulator tiles, rounded, as one 16-byte run: a lane has channels 4 lg .. of both, and after exchanging with the lane group beside it channels 8 (lg
+// / 2) .. of the one (even groups) or the other.
+__device__ __forceinline__ bf16x8 la_pair(f32x4 a, f32x4 b) {
+    typedef unsigned u2 __attribute__((ext_vector_type(2)));
+    typedef unsigned u4 __attribute__((ext_vector_type(4)));
+    const u2 x = __builtin_bit_cast(u2, bf16x4{(bf16)a[0], (bf16)a[1], (bf16)a[2], (bf16)a[3]});
+    const u2 y = __builtin_bit_cast(u2, bf16x4{(bf16)b[0], (bf16)b[1], (bf16)b[2], (bf16)b[3]});
+    const auto p = __builtin_amdgcn_permlane16_swap(x[0], y[0], false, false);
+    const auto q = __builtin_amdgcn_permlane16_swap(x[1], y[1], false, false);
+    return __builtin_bit_cast(bf16x8, u4{p[0], q[0], p[1], q[1]});
 }
 
-// Workgroup of four waves per (span, head).  SPLITS: bf16 terms per weighted c (1 for
-// float32).  `ws`: the spans' states, [slot][H][wave][tile][lane] f32x4.
+// One span of one head, by a workgroup of four waves.  SPLITS: bf16 terms per weighted c (1
+// for float32).  `ws`: the spans' states, [slot][H][wave][tile][lane] f32x4.
 //
 // A c_j that is not finite times a masked score's 0 would be NaN in the outputs before j.  A
 // chunk that has one puts 0 in its place, and NaN into the state and, from j on, the
 // outputs of its channel.  Both happen where few registers are live.
 template <typename T, int BD, int CD, bool REV, int OUT, int SPLITS>
-__global__ void __launch_bounds__(256, (la_waves<BD, CD, OUT>()))
-k_la_walk(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
+__device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
+                                        f32x4* __restrict__ ws, unsigned char* lds, int64_t slot,
+                                        int h) {
     typedef Mma<T> M;
     typedef typename M::Frag Frag;
     constexpr int Q = LaCfg<T>::Q, TPK = LaCfg<T>::TPK, NT = Q / 16, NK = NT / TPK;
     constexpr int SL = M::SL, KS = M::KS, KB = BD / KS;
     constexpr int BT = BD / 16, CW = CD / 4, CT = CW / 16;  // tiles of M^T of one wave
     constexpr int AP = LaRows<T, BD, REV>::PITCH, CP = LaRows<T, CD, REV>::PITCH;
-    __shared__ __align__(16) unsigned char lds[la_lds_bytes<T, BD, CD, OUT>()];
     T* sb = (T*)lds;
     T* sc = sb + Q * AP;
     T* sa = sc + Q * CP;
@@ -225,17 +231,6 @@ k_la_walk(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
     int* wild_row = wild + 4;               // the first such row of each channel, or Q
     if (OUT && threadIdx.x == 0) *wild = 0;
 
-    // The hardware deals workgroups out over the 8 XCDs in turn.  The heads that share keys
-    // and values go to one XCD, whose L2 then holds them; such groups, and with them the
-    // idle numbers, are spread over all (in contiguous ranges to an XCD, idle ones leave some
-    // XCDs with more spans than they have room for at once: 119 us instead of 8x us for the
-    // walk of 2 x 8192 tokens, 32 heads of 128 x 64).
-    const int share = w.share;
-    const int64_t unit = blockIdx.x / 8 / share * 8 + blockIdx.x % 8;
-    const int groups = w.H / share;
-    const int64_t slot = unit / groups;
-    if (slot >= plan.slots) return;
-    const int h = (int)(unit % groups) * share + (int)(blockIdx.x / 8 % share);
     const LaSpan sp_ = la_span(w, plan, slot);
     if (sp_.s < 0 || (!OUT && sp_.last)) return;
     const int wave = wave_id(), lane = threadIdx.x % 64, lr = lane % 16, lg = lane / 16;
@@ -360,39 +355,41 @@ k_la_walk(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
 
         f32x4 o[NT][CT];
         if constexpr (OUT) {
-            // scores of row tile `wave`: k blocks up to the diagonal
-            if (wave < NT) {
+            // The scores' k blocks up to the diagonal, (row tile, k block), dealt out evenly: of
+            // bf16's ten tiles three, three, two and two.
+            const int first = NT == 4 ? (wave < 2 ? 2 * wave : 3) : (wave > 0);
+            const int units = NT == 4 ? (wave < 2 ? 2 : 1) : (wave < 3);
+#pragma unroll 1
+            for (int x = 0; x < units; ++x) {
+                const int it = first + (NT == 4 && wave == 0 ? x : 0);
+                const int kb = NT == 4 ? (wave == 0 ? 0 : (wave == 1 ? x : wave - 2)) : wave == 2;
                 Frag af[KB];
 #pragma unroll
                 for (int q = 0; q < KB; ++q)
-                    af[q] = M::load(sa + (16 * wave + lr) * AP + KS * q + SL * lg);
+                    af[q] = M::load(sa + (16 * it + lr) * AP + KS * q + SL * lg);
+                f32x4 tl[TPK];
 #pragma unroll
-                for (int kb = 0; kb < NK; ++kb) {
-                    if (kb * TPK > wave) break;
-                    f32x4 tl[TPK];
+                for (int e = 0; e < TPK; ++e) {
+                    const int jt = kb * TPK + e;
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                    if (jt <= it) {
 #pragma unroll
-                    for (int e = 0; e < TPK; ++e) {
-                        const int jt = kb * TPK + e;
-                        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-                        if (jt <= wave) {
+                        for (int q = 0; q < KB; ++q)
+                            acc = M::mma(M::load(sb + (16 * jt + lr) * AP + KS * q + SL * lg),
+                                         af[q], acc);
+                        if (jt == it) {
 #pragma unroll
-                            for (int q = 0; q < KB; ++q)
-                                acc = M::mma(M::load(sb + (16 * jt + lr) * AP + KS * q + SL * lg),
-                                             af[q], acc);
-                            if (jt == wave) {
+                            for (int r = 0; r < 4; ++r)
+                                acc[r] = 4 * lg + r <= lr ? acc[r] * dg[r] : 0.f;
+                        } else {
+                            const float f = it - jt == 1 ? 1.f : (it - jt == 2 ? l16 : l32);
 #pragma unroll
-                                for (int r = 0; r < 4; ++r)
-                                    acc[r] = 4 * lg + r <= lr ? acc[r] * dg[r] : 0.f;
-                            } else {
-                                const float f = wave - jt == 1 ? 1.f : (wave - jt == 2 ? l16 : l32);
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) acc[r] *= lw[r] * f;
-                            }
+                            for (int r = 0; r < 4; ++r) acc[r] *= lw[r] * f;
                         }
-                        tl[e] = acc;
                     }
-                    sp[(wave * NK + kb) * 64 + lane] = la_frag<T>(tl);
+                    tl[e] = acc;
                 }
+                sp[(it * NK + kb) * 64 + lane] = la_frag<T>(tl);
             }
             if (*wild) {  // for the whole workgroup
                 tame = true;
@@ -490,20 +487,28 @@ k_la_walk(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
             // a lane holds channels 4 lg .. of row lr of every tile; rows without a token are
             // beyond the buffer's bound
             typedef typename std::conditional<OUT == LA_F32, float, T>::type OT;
-            typedef typename Vec4<OT>::type ov;
             const __amdgpu_buffer_rsrc_t r = buf_rsrc(
                 (OT*)w.out + first_token(k, n) * w.out_ts + (int64_t)h * CD, n * out_bytes);
+            auto row_at = [&](int i) { return (REV ? Q - 1 - i : i - (Q - n)) * out_bytes; };
+            if constexpr (sizeof(OT) == 2) {
+                const int half = lg & 1, c8 = wave * CW + 8 * (lg >> 1);
+                if constexpr (CT == 2) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int i = 16 * t + lr;
+                    for (int t = 0; t < NT; ++t)
+                        buf_store(la_pair(o[t][0], o[t][1]), r,
+                                  row_at(16 * t + lr) + (c8 + 16 * half) * 2);
+                } else {
 #pragma unroll
-                for (int u = 0; u < CT; ++u) {
-                    ov v;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] = (OT)o[t][u][c];
-                    buf_store(v, r, (REV ? Q - 1 - i : i - (Q - n)) * out_bytes +
-                                        (wave * CW + 16 * u + 4 * lg) * (int)sizeof(OT));
+                    for (int t = 0; t < NT; t += 2)
+                        buf_store(la_pair(o[t][0], o[t + 1][0]), r,
+                                  row_at(16 * (t + half) + lr) + c8 * 2);
                 }
+            } else {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int u = 0; u < CT; ++u)
+                        buf_store(o[t][u], r, row_at(16 * t + lr) + (wave * CW + 16 * u + 4 * lg) * 4);
             }
         }
         if (late && k == 0) {
@@ -552,6 +557,68 @@ k_la_walk(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
                 }
             }
     }
+}
+
+// What a workgroup of a launch works on.  The hardware deals workgroups out over the 8 XCDs
+// in turn.  Those that read the same rows (the walks of a backward, the heads that share
+// keys and values: `members` of them) go to one XCD, whose L2 then holds the rows; such
+// units, and with them the idle numbers, are spread over all.  (In contiguous ranges to an
+// XCD, idle ones leave some XCDs with more spans than they have room for at once: 119 us
+// instead of 88 us for the walk of 2 x 8192 tokens, 32 heads of 128 x 64.)
+struct LaItem {
+    int64_t slot;
+    int h, member;  // member / share: the walk
+};
+__device__ __forceinline__ LaItem la_item(const LaWalk& w, int members) {
+    const int64_t unit = (int64_t)(blockIdx.x / 8 / members) * 8 + blockIdx.x % 8;
+    const int groups = w.H / w.share;
+    LaItem i;
+    i.slot = unit / groups;
+    i.member = (int)(blockIdx.x / 8 % members);
+    i.h = (int)(unit % groups) * w.share + i.member % w.share;
+    return i;
+}
+inline dim3 la_grid(const LaWalk& w, const LaPlan& p, int members) {
+    const int64_t units = p.slots * (w.H / w.share);
+    return dim3((unsigned)((units + 7) / 8 * 8 * members));
+}
+
+// Waves per SIMD that the registers allow.
+template <int BD, int CD, int OUT>
+constexpr int la_waves() {
+    return BD + CD <= 128 || (OUT == LA_STATE && BD + CD <= 192) ? 3 : 2;
+}
+
+template <typename T, int BD, int CD, int OUT, int SPLITS>
+__global__ void __launch_bounds__(256, (la_waves<BD, CD, OUT>()))
+k_la_fwd(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
+    __shared__ __align__(16) unsigned char lds[la_lds_bytes<T, BD, CD, OUT>()];
+    const LaItem i = la_item(w, w.share);
+    if (i.slot < plan.slots) la_walk<T, BD, CD, false, OUT, SPLITS>(w, plan, ws, lds, i.slot, i.h);
+}
+
+// The three walks of the backward, DQ from the first token on, DV and DK from the last one
+// back, in one launch: dv and dk then read q and do at the same time, from one L2.
+enum { LA_DQ = 0, LA_DV = 1, LA_DK = 2 };
+struct LaBwd {
+    LaWalk w[3];
+    f32x4* ws[3];
+};
+template <typename T, int DK, int DV, int OUT, int SPLITS, int SPLITS_DV>
+__global__ void __launch_bounds__(256, (la_waves<DK, DV, OUT>()))
+k_la_bwd(LaBwd b, LaPlan plan) {
+    constexpr int LA = la_lds_bytes<T, DV, DK, OUT>(), LB = la_lds_bytes<T, DK, DV, OUT>();
+    __shared__ __align__(16) unsigned char lds[LA > LB ? LA : LB];
+    const LaItem i = la_item(b.w[0], 3 * b.w[0].share);
+    if (i.slot >= plan.slots) return;
+    const int walk = i.member / b.w[0].share;
+    constexpr int ODQ = OUT == LA_STATE ? LA_STATE : LA_ACT;
+    if (walk == LA_DQ)
+        la_walk<T, DV, DK, false, ODQ, SPLITS>(b.w[LA_DQ], plan, b.ws[LA_DQ], lds, i.slot, i.h);
+    else if (walk == LA_DV)
+        la_walk<T, DK, DV, true, OUT, SPLITS_DV>(b.w[LA_DV], plan, b.ws[LA_DV], lds, i.slot, i.h);
+    else
+        la_walk<T, DV, DK, true, OUT, SPLITS>(b.w[LA_DK], plan, b.ws[LA_DK], lds, i.slot, i.h);
 }
 
 }  // namespace ssd

@@ -7,10 +7,11 @@ namespace ssd {
 // States entering the spans of a sequence from the states its spans add: in place, slot
 // j >= 1 receives the state after span j - 1.  One lane per four state elements of a
 // (sequence, head).
-__global__ void __launch_bounds__(256) k_la_spans(LaWalk w, LaPlan plan, int quads,
-                                                 f32x4* __restrict__ ws) {
-    const int per = quads / 256, h = (int)(blockIdx.x / per % w.H);
-    const int s = (int)(blockIdx.x / per / w.H), q = (int)(blockIdx.x % per) * 256 + threadIdx.x;
+__device__ __forceinline__ void la_compose(const LaWalk& w, const LaPlan& plan,
+                                           f32x4* __restrict__ ws, int64_t block) {
+    const int quads = w.bd * w.cd / 4, per = quads / 256;
+    const int h = (int)(block / per % w.H), s = (int)(block / per / w.H);
+    const int q = (int)(block % per) * 256 + threadIdx.x;
     const SeqRange r = seq_range(w, s);
     const int64_t n = (r.hi - r.lo + plan.span - 1) / plan.span;
     if (n < 2) return;
@@ -26,77 +27,34 @@ __global__ void __launch_bounds__(256) k_la_spans(LaWalk w, LaPlan plan, int qua
         m = m * keep + add;
     }
 }
+__global__ void __launch_bounds__(256) k_la_spans(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
+    la_compose(w, plan, ws, blockIdx.x);
+}
+__global__ void __launch_bounds__(256) k_la_spans_bwd(LaBwd b, LaPlan plan) {
+    la_compose(b.w[blockIdx.y], plan, b.ws[blockIdx.y], blockIdx.x);
+}
 
+// out[t][hk][d] = sum over the group's heads of part[t][h][d], tokens of sequences only; four
+// channels to a lane.
+struct LaSum {
+    const float* part[2];
+    void* out[2];
+    int64_t out_ts[2];
+    int cd[2];
+};
 template <typename T>
-__global__ void __launch_bounds__(256) k_la_group_sum(LaWalk w, const float* __restrict__ part,
-                                                     int nkv, T* __restrict__ out, int64_t out_ts) {
+__global__ void __launch_bounds__(256) k_la_group_sum(LaWalk w, LaSum s) {
+    const int k = blockIdx.y, cd = s.cd[k], r = w.share, n = w.H / r * (cd / 4);
     const int64_t lo = seq_range(w, 0).lo, hi = seq_range(w, w.nseq - 1).hi;
-    const int r = w.H / nkv, n = nkv * w.cd;
-    const int64_t total = w.tokens * n;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const int64_t t = i / n;
-        const int hk = (int)(i % n) / w.cd, d = (int)(i % n) % w.cd;
-        if (t < lo || t >= hi) continue;
-        const float* p = part + (t * w.H + (int64_t)hk * r) * w.cd + d;
-        float s = 0.f;
-        for (int j = 0; j < r; ++j) s += p[(int64_t)j * w.cd];
-        out[t * out_ts + hk * w.cd + d] = (T)s;
+    typedef typename Vec4<T>::type vt;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < (hi - lo) * n; i += gridDim.x * 256ll) {
+        const int64_t t = lo + i / n;
+        const int c = (int)(i % n), hk = c / (cd / 4), d = c % (cd / 4) * 4;
+        const float* p = s.part[k] + (t * w.H + (int64_t)hk * r) * cd + d;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < r; ++j) v += *(const f32x4*)(p + (int64_t)j * cd);
+        *(vt*)((T*)s.out[k] + t * s.out_ts[k] + hk * cd + d) = vt{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
     }
-}
-
-// Spans: two workgroups for each of the 256 CUs where the tokens allow it, but none
-// shorter than 256 tokens (a span costs a state's round trip and a pass over b and c).
-constexpr int LA_BLOCKS = 512, LA_MIN_SPAN = 256;
-
-static LaPlan la_plan(const LaWalk& w) {
-    const int64_t per = (w.tokens * w.H + LA_BLOCKS - 1) / LA_BLOCKS;
-    LaPlan p;
-    p.span = (int)((per > LA_MIN_SPAN ? per + 63 : LA_MIN_SPAN) / 64 * 64);
-    p.per_row = (int)((w.seqlen + p.span - 1) / p.span);
-    p.slots = w.cu ? w.tokens / p.span + w.nseq : (int64_t)w.nseq * p.per_row;
-    p.split = (w.cu ? w.tokens : w.seqlen) > p.span;
-    return p;
-}
-
-size_t la_walk_ws(const LaWalk& w, int) {
-    const LaPlan p = la_plan(w);
-    return p.split ? (size_t)p.slots * w.H * w.bd * w.cd * 4 : 0;
-}
-
-template <typename T, int BD, int CD, bool REV>
-static hipError_t walk_shape(const LaWalk& w, f32x4* ws, hipStream_t s) {
-    constexpr int FINE = sizeof(T) == 2 ? 3 : 1, FAST = sizeof(T) == 2 ? 2 : 1;
-    const LaPlan p = la_plan(w);
-    const int64_t units = p.slots * (w.H / w.share);
-    const dim3 grid((unsigned)((units + 7) / 8 * 8 * w.share)), block(256);
-    if (p.split) {
-        SSD_TRY(launch(k_la_walk<T, BD, CD, REV, LA_STATE, FINE>, grid, block, s, w, p, ws));
-        constexpr int quads = BD * CD / 4;
-        SSD_TRY(launch(k_la_spans, dim3((unsigned)((int64_t)w.nseq * w.H * (quads / 256))),
-                       dim3(256), s, w, p, quads, ws));
-    }
-    if constexpr (REV)
-        if (w.out_f32) {
-            if (w.fin)
-                return launch(k_la_walk<T, BD, CD, REV, LA_F32, FINE>, grid, block, s, w, p, ws);
-            return launch(k_la_walk<T, BD, CD, REV, LA_F32, FAST>, grid, block, s, w, p, ws);
-        }
-    if (w.fin) return launch(k_la_walk<T, BD, CD, REV, LA_ACT, FINE>, grid, block, s, w, p, ws);
-    return launch(k_la_walk<T, BD, CD, REV, LA_ACT, FAST>, grid, block, s, w, p, ws);
-}
-
-template <typename T, bool REV>
-static hipError_t walk_dims(const LaWalk& w, f32x4* ws, hipStream_t s) {
-    if (w.bd == 64) return w.cd == 64 ? walk_shape<T, 64, 64, REV>(w, ws, s)
-                                      : walk_shape<T, 64, 128, REV>(w, ws, s);
-    return w.cd == 64 ? walk_shape<T, 128, 64, REV>(w, ws, s)
-                      : walk_shape<T, 128, 128, REV>(w, ws, s);
-}
-
-template <typename T>
-static hipError_t walk_t(const LaWalk& w, void* ws, hipStream_t s) {
-    return w.reverse ? walk_dims<T, true>(w, (f32x4*)ws, s)
-                     : walk_dims<T, false>(w, (f32x4*)ws, s);
 }
 
 bool la_supported(int keydim, int valdim, int act) {
@@ -104,17 +62,128 @@ bool la_supported(int keydim, int valdim, int act) {
            (act == SSD_F32 || act == SSD_BF16);
 }
 
-hipError_t launch_la_walk(const LaWalk& w, int act, void* ws, hipStream_t s) {
-    return act == SSD_BF16 ? walk_t<bf16>(w, ws, s) : walk_t<float>(w, ws, s);
+// Spans.  A sequence walked whole takes about a microsecond per 64 tokens; one walked in
+// spans takes two launches more, a second pass over b and c and a state's round trip per
+// span.  So: none up to LA_WHOLE tokens, then as many as give every CU two workgroups, but
+// none shorter than LA_MIN_SPAN.
+constexpr int LA_BLOCKS = 512, LA_MIN_SPAN = 256, LA_WHOLE = 1024;
+
+static LaPlan la_plan(const LaWalk& w, int walks) {
+    const int64_t longest = w.cu ? w.tokens : w.seqlen;  // cu_seqlens is on the device
+    const int64_t per = (w.tokens * w.H * walks + LA_BLOCKS - 1) / LA_BLOCKS;
+    LaPlan p;
+    p.split = longest > LA_WHOLE && longest > per;
+    const int64_t span = p.split ? (per > LA_MIN_SPAN ? per : LA_MIN_SPAN) : longest;
+    p.span = (int)((span + 63) / 64 * 64);
+    p.per_row = (int)((w.seqlen + p.span - 1) / p.span);
+    p.slots = w.cu ? w.tokens / p.span + w.nseq : (int64_t)w.nseq * p.per_row;
+    return p;
 }
 
-hipError_t launch_la_group_sum(const LaWalk& w, int act, const float* part, int nkv, void* out,
-                               int64_t out_ts, hipStream_t s) {
-    const int64_t n = (w.tokens * nkv * w.cd + 255) / 256;
-    const dim3 grid((unsigned)(n < 16384 ? n : 16384)), block(256);
-    if (act == SSD_BF16)
-        return launch(k_la_group_sum<bf16>, grid, block, s, w, part, nkv, (bf16*)out, out_ts);
-    return launch(k_la_group_sum<float>, grid, block, s, w, part, nkv, (float*)out, out_ts);
+static size_t state_ws(const LaWalk& w, const LaPlan& p) {
+    return p.split ? align256((size_t)p.slots * w.H * w.bd * w.cd * 4) : 0;
+}
+
+size_t la_fwd_ws(const LaWalk& w) { return state_ws(w, la_plan(w, 1)); }
+
+// Span states of the three walks, then, where heads share keys and values, dv and dk per
+// head in float32.
+size_t la_bwd_ws(const LaWalk& dv) {
+    size_t n = 3 * state_ws(dv, la_plan(dv, 3));
+    if (dv.share > 1) n += align256((size_t)dv.tokens * dv.H * (dv.bd + dv.cd) * 4);
+    return n;
+}
+
+template <typename T, int BD, int CD, int SPLITS>
+static hipError_t fwd_splits(const LaWalk& w, f32x4* ws, hipStream_t s) {
+    const LaPlan p = la_plan(w, 1);
+    const dim3 grid = la_grid(w, p, w.share), block(256);
+    if (p.split) {
+        SSD_TRY(launch(k_la_fwd<T, BD, CD, LA_STATE, SPLITS>, grid, block, s, w, p, ws));
+        SSD_TRY(launch(k_la_spans, dim3((unsigned)((int64_t)w.nseq * w.H * (BD * CD / 1024))),
+                       block, s, w, p, ws));
+    }
+    return launch(k_la_fwd<T, BD, CD, LA_ACT, SPLITS>, grid, block, s, w, p, ws);
+}
+
+template <typename T, int BD, int CD>
+static hipError_t fwd_dims(const LaWalk& w, f32x4* ws, hipStream_t s) {
+    if constexpr (sizeof(T) == 4) return fwd_splits<T, BD, CD, 1>(w, ws, s);
+    else return w.fin ? fwd_splits<T, BD, CD, 3>(w, ws, s) : fwd_splits<T, BD, CD, 2>(w, ws, s);
+}
+
+template <typename T>
+static hipError_t fwd_t(const LaWalk& w, f32x4* ws, hipStream_t s) {
+    if (w.bd == 64) return w.cd == 64 ? fwd_dims<T, 64, 64>(w, ws, s) : fwd_dims<T, 64, 128>(w, ws, s);
+    return w.cd == 64 ? fwd_dims<T, 128, 64>(w, ws, s) : fwd_dims<T, 128, 128>(w, ws, s);
+}
+
+hipError_t launch_la_fwd(const LaWalk& w, int act, void* ws, hipStream_t s) {
+    return act == SSD_BF16 ? fwd_t<bf16>(w, (f32x4*)ws, s) : fwd_t<float>(w, (f32x4*)ws, s);
+}
+
+template <typename T, int DK, int DV, int OUT, int SPLITS, int SPLITS_DV>
+static hipError_t bwd_splits(const LaBwd& b, hipStream_t s) {
+    const LaWalk& w = b.w[0];
+    const LaPlan p = la_plan(w, 3);
+    const dim3 grid = la_grid(w, p, 3 * w.share), block(256);
+    if (p.split) {
+        SSD_TRY(launch(k_la_bwd<T, DK, DV, LA_STATE, SPLITS, SPLITS_DV>, grid, block, s, b, p));
+        SSD_TRY(launch(k_la_spans_bwd,
+                       dim3((unsigned)((int64_t)w.nseq * w.H * (DK * DV / 1024)), 3), block, s, b, p));
+    }
+    return launch(k_la_bwd<T, DK, DV, OUT, SPLITS, SPLITS_DV>, grid, block, s, b, p);
+}
+
+template <typename T, int DK, int DV, int OUT>
+static hipError_t bwd_out(const LaBwd& b, hipStream_t s) {
+    if constexpr (sizeof(T) == 4) return bwd_splits<T, DK, DV, OUT, 1, 1>(b, s);
+    else if (b.w[LA_DV].fin) return bwd_splits<T, DK, DV, OUT, 2, 3>(b, s);
+    else return bwd_splits<T, DK, DV, OUT, 2, 2>(b, s);
+}
+
+template <typename T, int DK, int DV>
+static hipError_t bwd_dims(const LaBwd& b, hipStream_t s) {
+    if constexpr (sizeof(T) == 2)
+        if (b.w[0].share > 1) return bwd_out<T, DK, DV, LA_F32>(b, s);
+    return bwd_out<T, DK, DV, LA_ACT>(b, s);  // float32 parts are its own type
+}
+
+template <typename T>
+static hipError_t bwd_t(LaBwd b, void* ws, hipStream_t s) {
+    const LaWalk& dv = b.w[LA_DV];
+    const size_t st = state_ws(dv, la_plan(dv, 3));
+    for (int i = 0; i < 3; ++i) b.ws[i] = (f32x4*)((char*)ws + i * st);
+    const bool shared = dv.share > 1;
+    LaSum sum = {};
+    if (shared) {
+        float* part = (float*)((char*)ws + 3 * st);
+        for (int i = 0; i < 2; ++i) {
+            LaWalk& w = b.w[LA_DV + i];
+            sum.part[i] = part;
+            sum.out[i] = w.out;
+            sum.out_ts[i] = w.out_ts;
+            sum.cd[i] = w.cd;
+            w.out = part;
+            w.out_ts = (int64_t)w.H * w.cd;
+            part += w.tokens * w.out_ts;
+        }
+    }
+    const int dk = dv.bd, dvd = dv.cd;
+    if (dk == 64) SSD_TRY(dvd == 64 ? bwd_dims<T, 64, 64>(b, s) : bwd_dims<T, 64, 128>(b, s));
+    else SSD_TRY(dvd == 64 ? bwd_dims<T, 128, 64>(b, s) : bwd_dims<T, 128, 128>(b, s));
+    if (!shared) return hipSuccess;
+    const int64_t n = (dv.tokens * (dv.H / dv.share) * ((dk > dvd ? dk : dvd) / 4) + 255) / 256;
+    return launch(k_la_group_sum<T>, dim3((unsigned)(n < 4096 ? n : 4096), 2), dim3(256), s, dv, sum);
+}
+
+hipError_t launch_la_bwd(const LaWalk& dq, const LaWalk& dv, const LaWalk& dk, int act, void* ws,
+                         hipStream_t s) {
+    LaBwd b = {};
+    b.w[LA_DQ] = dq;
+    b.w[LA_DV] = dv;
+    b.w[LA_DK] = dk;
+    return act == SSD_BF16 ? bwd_t<bf16>(b, ws, s) : bwd_t<float>(b, ws, s);
 }
 
 }  // namespace ssd

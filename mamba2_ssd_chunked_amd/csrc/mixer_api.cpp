@@ -29,7 +29,7 @@ int check_linattn(const ssd_linattn* p, LaStrides* st) {
     if (p->nheads % p->nkvheads != 0 || p->nheads > 65535) return SSD_ERR_SHAPE;
     if (p->act_dtype != SSD_F32 && p->act_dtype != SSD_BF16) return SSD_ERR_UNSUPPORTED;
     if (!la_supported(p->keydim, p->valdim, p->act_dtype)) return SSD_ERR_UNSUPPORTED;
-    if (p->batch > INT32_MAX || p->seqlen > INT32_MAX || p->batch * p->seqlen > INT32_MAX)
+    if (p->batch > INT32_MAX || p->seqlen > INT32_MAX || p->batch * p->seqlen > INT32_MAX - 127)
         return SSD_ERR_SHAPE;
     const int64_t esz = p->act_dtype == SSD_BF16 ? 2 : 4;
     auto stride = [&](int64_t given, int64_t packed, int64_t* out) {
@@ -83,17 +83,15 @@ LaWalk fwd_walk(const ssd_linattn* p, const LaStrides& st, int32_t nseq, const v
     return w;
 }
 
-// The three walks of the backward: dq, dv, dk.  Where heads share keys and values, dv and
-// dk go to `part` as float32 per head first.
+// The three walks of the backward.
 struct BwdWalks {
     LaWalk dq, dv, dk;
 };
 BwdWalks bwd_walks(const ssd_linattn* p, const LaStrides& st, int32_t nseq, const void* q,
                    const void* k, const void* v, const float* log_decay, const int32_t* cu,
                    const void* dout, const float* init, const float* dfinal, void* dq, void* dk,
-                   void* dv, float* dinit, float* part) {
+                   void* dv, float* dinit) {
     const int div = p->nheads / p->nkvheads;
-    const int64_t H = p->nheads;
     BwdWalks b;
     LaWalk w = base_walk(p, nseq, log_decay, cu);
     w.a = dout, w.a_ts = st.o;
@@ -109,8 +107,7 @@ BwdWalks bwd_walks(const ssd_linattn* p, const LaStrides& st, int32_t nseq, cons
     w.b = q, w.b_ts = st.q;
     w.c = dout, w.c_ts = st.o;
     w.bd = p->keydim, w.cd = p->valdim;
-    w.out = div > 1 ? (void*)part : dv, w.out_ts = div > 1 ? H * p->valdim : st.dv;
-    w.out_f32 = div > 1;
+    w.out = dv, w.out_ts = st.dv;
     w.init = dfinal, w.fin = dinit;
     w.reverse = true;
     w.intra = w.state_scale = p->scale, w.inter = 1.f;
@@ -119,39 +116,30 @@ BwdWalks bwd_walks(const ssd_linattn* p, const LaStrides& st, int32_t nseq, cons
     w.b = dout, w.b_ts = st.o;
     w.c = q, w.c_ts = st.q;
     w.bd = p->valdim, w.cd = p->keydim;
-    w.out = div > 1 ? (void*)part : dk, w.out_ts = div > 1 ? H * p->keydim : st.dk;
+    w.out = dk, w.out_ts = st.dk;
     w.fin = nullptr, w.trans = true;
     b.dk = w;
     return b;
 }
 
-size_t part_bytes(const ssd_linattn* p) {
-    if (p->nheads == p->nkvheads) return 0;
-    const size_t d = p->keydim > p->valdim ? p->keydim : p->valdim;
-    return align256((size_t)(p->batch * p->seqlen) * p->nheads * d * 4);
-}
-
-size_t linattn_ws(const ssd_linattn* p, const LaStrides& st, int32_t nseq, int32_t kind) {
-    // the layout does not depend on the pointers
+size_t linattn_ws(const ssd_linattn* p, const LaStrides& st, int32_t nseq, const int32_t* cu,
+                  int32_t kind) {
+    // the layout depends on no other pointer
     if (kind == SSD_WS_FORWARD)
-        return la_walk_ws(fwd_walk(p, st, nseq, nullptr, nullptr, nullptr, nullptr, nullptr,
-                                   nullptr, nullptr, nullptr), p->act_dtype);
-    const BwdWalks b = bwd_walks(p, st, nseq, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
-                                 nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
-    size_t n = la_walk_ws(b.dq, p->act_dtype);
-    for (const LaWalk* w : {&b.dv, &b.dk}) {
-        const size_t m = la_walk_ws(*w, p->act_dtype);
-        n = m > n ? m : n;
-    }
-    return part_bytes(p) + n;
+        return la_fwd_ws(fwd_walk(p, st, nseq, nullptr, nullptr, nullptr, nullptr, cu, nullptr,
+                                  nullptr, nullptr));
+    return la_bwd_ws(bwd_walks(p, st, nseq, nullptr, nullptr, nullptr, nullptr, cu, nullptr,
+                               nullptr, nullptr, nullptr, nullptr, nullptr, nullptr).dv);
 }
 
-// Every launch of the walks fits: a workgroup per (span, head), spans of at least 256 tokens
-// (rounded up to 8 spans), and up to 16 per (sequence, head) to compose span states.
+// Every launch of the walks fits: up to three workgroups per (span, head), spans of at least
+// 256 tokens, their number rounded up to one of 8 XCDs, and up to 16 per (sequence, head)
+// to compose span states.
 int check_walk_grid(const ssd_linattn* p, int32_t nseq) {
     typedef unsigned __int128 u128;
     const u128 spans = (u128)(p->batch * p->seqlen) / 256 + nseq;
-    const u128 blocks = (spans + 8 > (u128)nseq * 16 ? spans + 8 : (u128)nseq * 16) * p->nheads;
+    const u128 blocks = (3 * (spans + 8) > (u128)nseq * 16 ? 3 * (spans + 8) : (u128)nseq * 16) *
+                        p->nheads;
     return blocks <= (u128)MAX_BLOCKS ? SSD_OK : SSD_ERR_SHAPE;
 }
 
@@ -200,9 +188,12 @@ size_t ssd_linattn_workspace_bytes(const ssd_linattn* problem, int32_t nseq, int
     if (check_linattn(problem, &st) != SSD_OK) return 0;
     if (nseq < 1 || nseq > (1 << 24) || check_walk_grid(problem, nseq) != SSD_OK) return 0;
     if (kind != SSD_WS_FORWARD && kind != SSD_WS_BACKWARD) return 0;
-    // never 0 for a valid problem, which 0 would call invalid
-    const size_t n = linattn_ws(problem, st, nseq, kind);
-    return n ? n : 256;
+    // rows or packed sequences, whichever needs more (a batch of one row may be either)
+    const int32_t packed = 0;
+    const size_t m = linattn_ws(problem, st, nseq, nullptr, kind);
+    size_t n = problem->batch == 1 ? linattn_ws(problem, st, nseq, &packed, kind) : m;
+    if (m > n) n = m;
+    return n ? n : 256;  // 0 would say that the problem is invalid
 }
 
 int ssd_linattn_fwd(const ssd_linattn* problem, int32_t nseq, const void* q, const void* k,
@@ -215,14 +206,14 @@ int ssd_linattn_fwd(const ssd_linattn* problem, int32_t nseq, const void* q, con
     if ((rc = check_sequences(problem, nseq, cu_seqlens))) return rc;
     if ((rc = check_walk_grid(problem, nseq))) return rc;
     if (!q || !k || !v || !log_decay || !o) return SSD_ERR_NULL;
-    if (!ws || ws_bytes < linattn_ws(problem, st, nseq, SSD_WS_FORWARD)) return SSD_ERR_WORKSPACE;
+    if (!ws || ws_bytes < linattn_ws(problem, st, nseq, cu_seqlens, SSD_WS_FORWARD)) return SSD_ERR_WORKSPACE;
     for (const void* x : {q, k, v, (const void*)init, (const void*)o, (const void*)final_state,
                           (const void*)ws})
         if (!aligned(x, 16)) return SSD_ERR_ALIGN;
     if (!aligned(log_decay, 4) || !aligned(cu_seqlens, 4)) return SSD_ERR_ALIGN;
     const LaWalk w = fwd_walk(problem, st, nseq, q, k, v, log_decay, cu_seqlens, init, o,
                               final_state);
-    return hip_status(launch_la_walk(w, problem->act_dtype, ws, (hipStream_t)stream));
+    return hip_status(launch_la_fwd(w, problem->act_dtype, ws, (hipStream_t)stream));
 }
 
 int ssd_linattn_bwd(const ssd_linattn* problem, int32_t nseq, const void* q, const void* k,
@@ -235,28 +226,14 @@ int ssd_linattn_bwd(const ssd_linattn* problem, int32_t nseq, const void* q, con
     if ((rc = check_sequences(problem, nseq, cu_seqlens))) return rc;
     if ((rc = check_walk_grid(problem, nseq))) return rc;
     if (!q || !k || !v || !log_decay || !dout || !dq || !dk || !dv) return SSD_ERR_NULL;
-    if (!ws || ws_bytes < linattn_ws(problem, st, nseq, SSD_WS_BACKWARD)) return SSD_ERR_WORKSPACE;
+    if (!ws || ws_bytes < linattn_ws(problem, st, nseq, cu_seqlens, SSD_WS_BACKWARD)) return SSD_ERR_WORKSPACE;
     for (const void* x : {q, k, v, dout, (const void*)init, (const void*)dfinal, (const void*)dq,
                           (const void*)dk, (const void*)dv, (const void*)dinit, (const void*)ws})
         if (!aligned(x, 16)) return SSD_ERR_ALIGN;
     if (!aligned(log_decay, 4) || !aligned(cu_seqlens, 4)) return SSD_ERR_ALIGN;
-    const int act = problem->act_dtype;
-    const hipStream_t s = (hipStream_t)stream;
-    float* part = (float*)ws;
-    void* walk_ws = (char*)ws + part_bytes(problem);
     const BwdWalks b = bwd_walks(problem, st, nseq, q, k, v, log_decay, cu_seqlens, dout, init,
-                                 dfinal, dq, dk, dv, dinit, part);
-    const bool shared = problem->nheads != problem->nkvheads;
-    if ((rc = hip_status(launch_la_walk(b.dq, act, walk_ws, s)))) return rc;
-    if ((rc = hip_status(launch_la_walk(b.dv, act, walk_ws, s)))) return rc;
-    if (shared && (rc = hip_status(launch_la_group_sum(b.dv, act, part, problem->nkvheads, dv,
-                                                       st.dv, s))))
-        return rc;
-    if ((rc = hip_status(launch_la_walk(b.dk, act, walk_ws, s)))) return rc;
-    if (shared && (rc = hip_status(launch_la_group_sum(b.dk, act, part, problem->nkvheads, dk,
-                                                       st.dk, s))))
-        return rc;
-    return SSD_OK;
+                                 dfinal, dq, dk, dv, dinit);
+    return hip_status(launch_la_bwd(b.dq, b.dv, b.dk, problem->act_dtype, ws, (hipStream_t)stream));
 }
 
 int ssd_linattn_step(const ssd_linattn* problem, const void* q, const void* k, const void* v,

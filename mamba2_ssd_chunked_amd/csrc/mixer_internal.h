@@ -34,7 +34,6 @@ struct LaWalk {
     int bd, cd;                      // channels per head of b (and a), of c (and out)
     void* out;                       // [tokens][H][cd]
     int64_t out_ts;
-    bool out_f32;                    // out is float32 (partial sums per head)
     const float* log_decay;          // [H]
     const int32_t* cu;               // [nseq + 1] or null (rows of `seqlen` tokens)
     int nseq;
@@ -66,11 +65,12 @@ __device__ __forceinline__ SeqRange seq_range(const LaWalk& w, int s) {
     return r;
 }
 
-size_t la_walk_ws(const LaWalk& w, int act);
-hipError_t launch_la_walk(const LaWalk& w, int act, void* ws, hipStream_t s);
-// out[t][hk][d] = sum over the group's heads of part[t][h][d], tokens of sequences only
-hipError_t launch_la_group_sum(const LaWalk& w, int act, const float* part, int nkv, void* out,
-                               int64_t out_ts, hipStream_t s);
+size_t la_fwd_ws(const LaWalk& w);
+size_t la_bwd_ws(const LaWalk& dv);  // the dv walk
+hipError_t launch_la_fwd(const LaWalk& w, int act, void* ws, hipStream_t s);
+// dv and dk hold the gradients' own tensors, also where heads share keys and values
+hipError_t launch_la_bwd(const LaWalk& dq, const LaWalk& dv, const LaWalk& dk, int act, void* ws,
+                         hipStream_t s);
 bool la_supported(int keydim, int valdim, int act);
 
 struct LaStep {
