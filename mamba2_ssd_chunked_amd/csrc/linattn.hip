@@ -64,17 +64,39 @@ bool la_supported(int keydim, int valdim, int act) {
 
 // Spans.  A sequence walked whole takes about a microsecond per 64 tokens; one walked in
 // spans takes two launches more, a second pass over b and c and a state's round trip per
-// span.  So: none up to LA_WHOLE tokens, then as many as give every CU two workgroups, but
-// none shorter than LA_MIN_SPAN.
-constexpr int LA_BLOCKS = 512, LA_MIN_SPAN = 256, LA_WHOLE = 1024;
+// span.  So: none up to LA_WHOLE tokens.  Longer rows are cut into the n spans that should
+// take the least time, counted in tokens that a workgroup walks one after the other: the
+// launch needs ceil(workgroups / LA_ROOM) turns of the CUs' room (two workgroups each), the
+// pass before it, over all spans but the last, 0.55 of that per token (51 against 88 us for
+// 2 x 8192 tokens, 32 heads of 128 x 64), and the rest about 256 tokens and a 64th of a span
+// for each.  (Three walks of those rows in 3 spans of 2731 tokens, 576 workgroups in two
+// turns: 414 us; in 8 of 1024, 1536 in three: 394 us.)  Packed sequences have their
+// lengths on the device: their tokens are cut as if into one row, but at least into two
+// turns' worth, since they fill the turns unevenly.
+constexpr int LA_ROOM = 512, LA_MIN_SPAN = 256, LA_WHOLE = 1024;
 
 static LaPlan la_plan(const LaWalk& w, int walks) {
-    const int64_t longest = w.cu ? w.tokens : w.seqlen;  // cu_seqlens is on the device
-    const int64_t per = (w.tokens * w.H * walks + LA_BLOCKS - 1) / LA_BLOCKS;
+    const int64_t longest = w.cu ? w.tokens : w.seqlen;
+    const int64_t rows = w.cu ? 1 : w.nseq, per = rows * w.H * walks;  // workgroups per span
+    auto turns = [](int64_t blocks) { return (double)((blocks + LA_ROOM - 1) / LA_ROOM); };
+    int64_t best = 1;
+    if (longest > LA_WHOLE) {
+        double least = turns(per) * (double)longest;
+        const int64_t most = (longest + LA_MIN_SPAN - 1) / LA_MIN_SPAN;
+        for (int64_t n = 2; n <= (most < 256 ? most : 256); ++n) {
+            const double span = (double)((longest + n - 1) / n);
+            const double t = turns(per * n) * span + 0.55 * turns(per * (n - 1)) * span + 256.0 +
+                             (double)n * 16.0;
+            if (t < least) least = t, best = n;
+        }
+        if (w.cu) {
+            const int64_t n = 2 * LA_ROOM / per;
+            if (n > best) best = n < most ? n : most;
+        }
+    }
     LaPlan p;
-    p.split = longest > LA_WHOLE && longest > per;
-    const int64_t span = p.split ? (per > LA_MIN_SPAN ? per : LA_MIN_SPAN) : longest;
-    p.span = (int)((span + 63) / 64 * 64);
+    p.split = best > 1;
+    p.span = (int)(((longest + best - 1) / best + 63) / 64 * 64);
     p.per_row = (int)((w.seqlen + p.span - 1) / p.span);
     p.slots = w.cu ? w.tokens / p.span + w.nseq : (int64_t)w.nseq * p.per_row;
     return p;
