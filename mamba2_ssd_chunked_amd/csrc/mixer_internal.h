@@ -120,19 +120,25 @@ hipError_t launch_norm_fwd(const NormArgs& a, int act, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, int act, float* part, hipStream_t s);
 
 // ---- serving helpers ---------------------------------------------------------------
-// Slot of row r, or -1 where the row is skipped: a slot outside the pool, a negative
-// position, or a slot that an earlier row already has.  All lanes of the wave call it and
-// agree.
+// Slot of row r, or -1 where the row is skipped: a slot outside the pool or a negative
+// position.
 __device__ __forceinline__ int64_t row_slot(const int32_t* slots, const int32_t* positions,
-                                            int64_t nslots, int r, int lane) {
+                                            int64_t nslots, int r) {
     if (positions && positions[r] < 0) return -1;
     if (!slots) return r;
     const int slot = __builtin_amdgcn_readfirstlane(slots[r]);
-    if (slot < 0 || slot >= nslots) return -1;
+    return slot < 0 || slot >= nslots ? -1 : slot;
+}
+// Whether an earlier row that is not skipped has row r's slot: then row r is.  All lanes of
+// the wave call it and agree.  (Called with the state's loads on their way: the scan of up to
+// r slots takes no longer than they do.)
+__device__ __forceinline__ bool row_taken(const int32_t* slots, const int32_t* positions,
+                                          int64_t slot, int r, int lane) {
+    if (!slots) return false;
     bool seen = false;
     for (int i = lane; i < r; i += 64)
         seen = seen || (slots[i] == slot && (!positions || positions[i] >= 0));
-    return __ballot(seen) ? -1 : slot;
+    return __ballot(seen) != 0;
 }
 
 }  // namespace ssd

@@ -36,14 +36,26 @@ _MODE = {"none": SSD_NORM_NONE, "silu": SSD_NORM_SILU, "before": SSD_NORM_BEFORE
 # ------------------------------------------------------------------ argument checks
 
 
+_calls = {}  # entry points by name, once the library is loaded
+
+
+def _entry(fn):
+    f = _calls.get(fn)
+    if f is None:
+        f = _calls[fn] = getattr(_lib.load(), fn)
+    return f
+
+
 class _Args:
     """The checked tensors of one call: all of them on one device."""
+
+    __slots__ = ("act", "device")
 
     def __init__(self, act):
         self.act = _TORCH_ACT[act]
         self.device = None
 
-    def _base(self, t, name, dtype):
+    def _base(self, t, name, dtype, shape):
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} is required")
         if not t.is_cuda:
@@ -52,28 +64,26 @@ class _Args:
             self.device = t.device
         elif t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, other tensors on {self.device}")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
     def flat(self, t, name, shape, dtype=torch.float32, optional=False):
         """A contiguous tensor of the given shape."""
         if t is None and optional:
             return None
-        self._base(t, name, dtype)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        self._base(t, name, dtype, shape)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
 
     def tokens(self, t, name, shape) -> Tuple[int, int]:
-        """(pointer, elements between tokens) of an activation tensor [batch, tokens,
+        """(pointer, elements between tokens; 0 packed) of an activation tensor [batch, tokens,
         *channels] whose channels are contiguous and whose rows follow each other."""
-        self._base(t, name, self.act)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        self._base(t, name, self.act, shape)
         if t.is_contiguous():
-            return t.data_ptr(), math.prod(shape[2:])
+            return t.data_ptr(), 0
         st, want = t.stride(), 1
         for n, s in zip(reversed(shape[2:]), reversed(st[2:])):
             if n > 1 and s != want:
@@ -97,14 +107,14 @@ class _Args:
         """The library call on the tensors' device; the stream comes last."""
         dev = self.device
         if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        f = getattr(_lib.load(), fn)
+            handle = torch._C._cuda_getCurrentRawStream(dev.index)
+        else:
+            handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         if dev.index == torch.cuda.current_device():
-            rc = f(*args, handle)
+            rc = _entry(fn)(*args, handle)
         else:
             with torch.cuda.device(dev):
-                rc = f(*args, handle)
+                rc = _entry(fn)(*args, handle)
         if rc != 0:
             raise SSDError(fn, rc)
 
@@ -139,12 +149,10 @@ def make_linattn(*, batch: int, seqlen: int, nheads: int, keydim: int, valdim: i
                    _act_code(act), keydim ** -0.5 if scale is None else scale)
 
 
-def _strided(p: LinAttn, **strides) -> LinAttn:
+def _strided(p: LinAttn, *strides) -> LinAttn:
     """The problem with the tensors' strides (a copy: the caller's stays as it is)."""
-    q = LinAttn.from_buffer_copy(p)
-    for k, v in strides.items():
-        setattr(q, k, v)
-    return q
+    return LinAttn(p.batch, p.seqlen, p.nheads, p.nkvheads, p.keydim, p.valdim, p.act_dtype,
+                   p.scale, *strides)
 
 
 def _nseq(p: LinAttn, cu_seqlens) -> int:
@@ -156,7 +164,7 @@ def _state_shape(p: LinAttn, n: int):
 
 
 def ssd_linattn_workspace_bytes(problem: LinAttn, nseq: int, kind: int = SSD_WS_FORWARD) -> int:
-    return int(_lib.load().ssd_linattn_workspace_bytes(ctypes.byref(problem), nseq, kind))
+    return int(_entry("ssd_linattn_workspace_bytes")(ctypes.byref(problem), nseq, kind))
 
 
 def ssd_linattn_fwd(problem: LinAttn, q, k, v, log_decay, cu_seqlens, init, o, final_state, ws,
@@ -173,7 +181,7 @@ def ssd_linattn_fwd(problem: LinAttn, q, k, v, log_decay, cu_seqlens, init, o, f
     ini = a.flat(init, "init", _state_shape(p, n), optional=True)
     fin = a.flat(final_state, "final_state", _state_shape(p, n), optional=True)
     wp, wn = a.scratch(ws, "ws")
-    p = _strided(p, q_stride=qs, k_stride=ks, v_stride=vs, o_stride=os_)
+    p = _strided(p, qs, ks, vs, os_)
     a.call("ssd_linattn_fwd", stream, ctypes.byref(p), n, qp, kp, vp, ld, cu, ini, op, fin, wp, wn)
 
 
@@ -192,7 +200,7 @@ def ssd_linattn_bwd(problem: LinAttn, q, k, v, log_decay, cu_seqlens, do, init, 
     ini, dfin = a.flat(init, "init", st, optional=True), a.flat(dfinal, "dfinal", st, optional=True)
     dini = a.flat(dinit, "dinit", st, optional=True)
     wp, wn = a.scratch(ws, "ws")
-    p = _strided(p, **{("o" if name == "do" else name) + "_stride": x[1] for name, x in t.items()})
+    p = _strided(p, *(t[name][1] for name in ("q", "k", "v", "do", "dq", "dk", "dv")))
     a.call("ssd_linattn_bwd", stream, ctypes.byref(p), n, t["q"][0], t["k"][0], t["v"][0], ld, cu,
            t["do"][0], ini, dfin, t["dq"][0], t["dk"][0], t["dv"][0], dini, wp, wn)
 
@@ -214,7 +222,7 @@ def ssd_linattn_step(problem: LinAttn, q, k, v, log_decay, state, o, slots=None,
     sp = a.flat(state, "state", _state_shape(p, state.shape[0]))
     sl = a.flat(slots, "slots", (b,), torch.int32, optional=True)
     po = a.flat(positions, "positions", (b,), torch.int32, optional=True)
-    p = _strided(p, q_stride=qs, k_stride=ks, v_stride=vs, o_stride=os_)
+    p = _strided(p, qs, ks, vs, os_)
     a.call("ssd_linattn_step", stream, ctypes.byref(p), qp, kp, vp, ld, sl, state.shape[0], po, sp,
            op)
 
@@ -370,10 +378,7 @@ def make_norm(*, rows: int, channels: int, act: str | int, ngroups: int = 1,
 
 
 def _norm_rows(a: _Args, t, name, p: Norm):
-    a._base(t, name, a.act)
-    shape = (p.rows, p.channels)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    a._base(t, name, a.act, (p.rows, p.channels))
     if p.channels > 1 and t.stride(1) != 1:
         raise ValueError(f"the channels of a row of {name} must be contiguous")
     step = t.stride(0) if p.rows > 1 else p.channels
@@ -408,7 +413,7 @@ def ssd_norm_fwd(problem: Norm, x, z, weight, bias, y, stream=None):
 
 
 def ssd_norm_workspace_bytes(problem: Norm) -> int:
-    return int(_lib.load().ssd_norm_workspace_bytes(ctypes.byref(problem)))
+    return int(_entry("ssd_norm_workspace_bytes")(ctypes.byref(problem)))
 
 
 def ssd_norm_bwd(problem: Norm, x, z, weight, bias, dy, dx, dz, dweight, dbias, ws, stream=None):

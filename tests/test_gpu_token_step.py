@@ -183,3 +183,30 @@ def test_captured_steps_follow_their_inputs():
         torch.cuda.synchronize()
         for n in ("y", "ring", "state"):
             assert torch.equal(e[n], c[n]), (i, n)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_many_rows_equal_few(act):
+    """A batch large enough to put two heads into one workgroup gives each row what a call
+    with that row alone gives, bit for bit."""
+    import mamba2_ssd_chunked_amd as ssd
+    rows, H, G, P, N = 300, 8, 2, 64, 64
+    x = draws(rows, 1, H, G, P, N, 4, act, rows, 4, seed=9)
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda") % 7
+    want = {n: x[n].clone() for n in ("conv_ring", "state")}
+
+    def step(r, n, ring, state, y):
+        p = ssd.make_problem(batch=n, seqlen=1, nheads=H, headdim=P, dstate=N, ngroups=G, chunk=64,
+                             conv_width=4, act=act)
+        ssd.ssd_token_step(p, x["xBC"][r:r + n], x["conv_w"], x["dt_raw"][r:r + n], x["dt_bias"],
+                           x["A_log"], x["D"], ring, state, pos[r:r + n].clone(), y)
+
+    y = torch.empty(rows, 1, H, P, dtype=ACT[act], device="cuda")
+    step(0, rows, x["conv_ring"], x["state"], y)
+    for r in (0, 1, 77, 151, 299):
+        yr = torch.empty(1, 1, H, P, dtype=ACT[act], device="cuda")
+        step(r, 1, want["conv_ring"][r:r + 1], want["state"][r:r + 1], yr)
+        torch.cuda.synchronize()
+        assert torch.equal(yr[0], y[r])
+        for n in want:
+            assert torch.equal(want[n][r], x[n][r]), (r, n)

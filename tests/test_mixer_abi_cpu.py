@@ -210,7 +210,7 @@ def _meta(shape, stride=None):
 
 
 @pytest.mark.parametrize("shape,stride,want", [
-    ((2, 8, 4, 16), None, 64),
+    ((2, 8, 4, 16), None, 0),                   # packed
     ((2, 8, 4, 16), (800, 100, 16, 1), 100),
     ((1, 8, 4, 16), (1, 100, 16, 1), 100),      # one row: its stride says nothing
     ((2, 1, 4, 16), (96, 1, 16, 1), 96),        # one token: the next row is the next token
@@ -221,7 +221,7 @@ def _meta(shape, stride=None):
 ])
 def test_token_layouts(shape, stride, want, monkeypatch):
     from mamba2_ssd_chunked_amd import mixer
-    monkeypatch.setattr(mixer._Args, "_base", lambda self, t, name, dtype: None)
+    monkeypatch.setattr(mixer._Args, "_base", lambda self, t, name, dtype, shape: None)
     a = mixer._Args(ssd.SSD_F32)
     t = _meta(shape, stride)
     if want is None:
