@@ -16,7 +16,8 @@
  *    (a slice of a projection's output): strides are in elements between tokens,
  *    0 means packed; the channels of a token are contiguous, and rows of a batch
  *    follow each other at seqlen times the token stride.
- *  - Nothing is read or written behind the last sequence, nor for a skipped row.
+ *  - Nothing is written behind the last sequence, nor for a skipped row.
+ *  - Outputs do not overlap inputs or each other, except where an entry point says so.
  *  - Results do not depend on the order in which workgroups run: every sum has a
  *    fixed order, no floating-point atomics.
  *  - No call keeps anything for the next one; a workspace is only used between the
@@ -40,7 +41,13 @@ extern "C" {
  *   o_t = scale S_t q_t
  * log_decay <= 0 is meant (minus infinity: every token sees itself alone); larger
  * values are not refused, the state then grows without bound.  The decays are
- * constants of the model: the backward gives no gradient for them. */
+ * constants of the model: the backward gives no gradient for them.
+ *
+ * Sums, states and decays are float32; a bf16 product's other operand is rounded to
+ * bf16 where it is a score or a state that enters an output, and taken in parts good to
+ * 2^-24 (2^-17 where no state is asked for) where it enters a state.  A value of q, k, v
+ * or do that is not finite reaches no other sequence and no output before it (backwards:
+ * behind it); its channel's states and later outputs are then NaN. */
 typedef struct {
     int64_t batch;      /* rows; 1 with cu_seqlens                               */
     int64_t seqlen;     /* tokens per row (with cu_seqlens: all tokens)          */

@@ -9,8 +9,8 @@
 // Bound by HBM: x, z (and dy) read once, y (dx, dz) written once.  A group of a row is held
 // in registers by a team of lanes between its statistics and its outputs; a team keeps one
 // group for all its rows, so that weight and bias, and the sums of dweight and dbias, stay
-// in registers too.  Groups too wide for a team, or not in whole 16-byte vectors, take the
-// kernels that read a group again for every sweep (k_norm_*_any).
+// in registers too.  Groups too wide for a team take the kernels that read a group again for
+// every sweep (k_norm_*_any).
 #include "mixer_internal.h"
 
 namespace ssd {
@@ -155,10 +155,19 @@ __global__ void __launch_bounds__(256) k_norm_bwd_any(NormArgs a, float* __restr
 
 constexpr int NORM_NT = 512;
 
-template <typename T>
+// E channels at a time: 16 bytes where groups and tensors are aligned to it, otherwise two
+// bf16, otherwise one channel (which still makes runs of whole cache lines for a wave).
+template <typename T, int E>
 struct NormVec {
-    static constexpr int E = 16 / (int)sizeof(T);
     typedef T type __attribute__((ext_vector_type(E)));
+};
+template <typename T>
+struct NormVec<T, 1> {
+    struct type {
+        T v;
+        __device__ __forceinline__ T& operator[](int) { return v; }
+        __device__ __forceinline__ const T& operator[](int) const { return v; }
+    };
 };
 
 // Team sums of N values at once.  With WIDE every team of the workgroup calls it.
@@ -186,9 +195,13 @@ __device__ __forceinline__ void team_sum(float (&v)[N], int lpt, float (*red)[NO
 // computed again, not held.
 template <typename V>
 __device__ __forceinline__ V forget(V v) {
-    f32x4 h = __builtin_bit_cast(f32x4, v);
-    asm volatile("" : "+v"(h));
-    return __builtin_bit_cast(V, h);
+    if constexpr (sizeof(V) == 16) {
+        f32x4 h = __builtin_bit_cast(f32x4, v);
+        asm volatile("" : "+v"(h));
+        return __builtin_bit_cast(V, h);
+    } else {
+        return v;
+    }
 }
 
 struct NormTeam {
@@ -197,7 +210,7 @@ struct NormTeam {
     int c0, nv;          // the group's first channel and its vectors
     int turns;           // (row, group)s of the team, with WIDE of the workgroup's busiest
 };
-template <typename T, bool WIDE>
+template <typename T, int E, bool WIDE>
 __device__ __forceinline__ NormTeam norm_team(const NormArgs& a, int lpt) {
     NormTeam t;
     t.lpt = lpt;
@@ -206,7 +219,7 @@ __device__ __forceinline__ NormTeam norm_team(const NormArgs& a, int lpt) {
     t.item = (int64_t)blockIdx.x * per + threadIdx.x / t.lpt;
     t.step = (int64_t)gridDim.x * per;  // a multiple of G: the group stays
     t.c0 = (int)(t.item % a.G) * a.gs;
-    t.nv = a.gs / NormVec<T>::E;
+    t.nv = a.gs / E;
     // the same for all teams of the workgroup, which meet in team_sum
     t.turns = (int)((a.rows * a.G - t.item + t.step - 1) / t.step);
     if (WIDE) {
@@ -217,10 +230,9 @@ __device__ __forceinline__ NormTeam norm_team(const NormArgs& a, int lpt) {
 }
 
 // weight or bias of the lane's channels; `otherwise` where there is none
-template <typename T, int EPL>
+template <int E, int EPL>
 __device__ __forceinline__ void norm_params(const float* p, const NormTeam& t, float otherwise,
                                             float (&o)[EPL]) {
-    constexpr int E = NormVec<T>::E;
 #pragma unroll
     for (int i = 0; i < EPL / E; ++i) {
         const int v = t.lane + i * t.lpt;
@@ -229,11 +241,10 @@ __device__ __forceinline__ void norm_params(const float* p, const NormTeam& t, f
     }
 }
 
-template <typename T, int EPL>
+template <typename T, int E, int EPL>
 __device__ __forceinline__ void norm_load(const T* row, const NormTeam& t,
-                                          typename NormVec<T>::type (&o)[EPL / NormVec<T>::E]) {
-    typedef typename NormVec<T>::type vt;
-    constexpr int E = NormVec<T>::E;
+                                          typename NormVec<T, E>::type (&o)[EPL / E]) {
+    typedef typename NormVec<T, E>::type vt;
 #pragma unroll
     for (int i = 0; i < EPL / E; ++i) {
         const int v = t.lane + i * t.lpt;
@@ -242,16 +253,15 @@ __device__ __forceinline__ void norm_load(const T* row, const NormTeam& t,
 }
 
 // u, then n = (u - m) r, of the lane's channels (0 where it has none); returns r
-template <typename T, int EPL, int MODE, bool WIDE, bool TIGHT = false>
+template <typename T, int E, int EPL, int MODE, bool WIDE, bool TIGHT = false>
 __device__ __forceinline__ float norm_n(const NormArgs& a, const NormTeam& t,
-                                        const typename NormVec<T>::type (&x)[EPL / NormVec<T>::E],
-                                        const typename NormVec<T>::type (&z)[EPL / NormVec<T>::E],
+                                        const typename NormVec<T, E>::type (&x)[EPL / E],
+                                        const typename NormVec<T, E>::type (&z)[EPL / E],
                                         float (&n)[EPL], float (*red)[NORM_NT / 64]) {
-    constexpr int E = NormVec<T>::E;
     const float inv = 1.f / (float)a.gs;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        if (TIGHT && i % E == 0) __builtin_amdgcn_sched_barrier(0);
+        if (TIGHT && i % 8 == 0) __builtin_amdgcn_sched_barrier(0);
         n[i] = (float)x[i / E][i % E];
         if (MODE == SSD_NORM_BEFORE) {
             const float zv = (float)z[i / E][i % E];
@@ -278,26 +288,26 @@ __device__ __forceinline__ float norm_n(const NormArgs& a, const NormTeam& t,
     return r;
 }
 
-template <typename T, int EPL, int MODE, bool WIDE>
+template <typename T, int E, int EPL, int MODE, bool WIDE>
 __global__ void __launch_bounds__(NORM_NT) k_norm_fwd(NormArgs a, int lpt) {
-    typedef typename NormVec<T>::type vt;
-    constexpr int E = NormVec<T>::E, V = EPL / E;
+    typedef typename NormVec<T, E>::type vt;
+    constexpr int V = EPL / E;
     constexpr bool GATED = MODE >= SSD_NORM_BEFORE;
     __shared__ float red[1][NORM_NT / 64];
-    const NormTeam t0 = norm_team<T, WIDE>(a, lpt);
+    const NormTeam t0 = norm_team<T, E, WIDE>(a, lpt);
     float w[EPL], b[EPL];
-    norm_params<T, EPL>(a.w, t0, 0.f, w);
-    norm_params<T, EPL>(a.b, t0, 0.f, b);
+    norm_params<E, EPL>(a.w, t0, 0.f, w);
+    norm_params<E, EPL>(a.b, t0, 0.f, b);
     NormTeam t = t0;
     for (int k = 0; k < t0.turns; ++k) {
         const int64_t it = t0.item + k * t0.step;
         if (WIDE && it >= a.rows * a.G) t.nv = 0;  // nothing to load or store, only to meet
         const int64_t row = WIDE && t.nv == 0 ? 0 : (uint32_t)it / (uint32_t)a.G;
         vt x[V], z[V];
-        norm_load<T, EPL>((const T*)a.x + row * a.xs + t.c0, t, x);
-        if (GATED) norm_load<T, EPL>((const T*)a.z + row * a.zs + t.c0, t, z);
+        norm_load<T, E, EPL>((const T*)a.x + row * a.xs + t.c0, t, x);
+        if (GATED) norm_load<T, E, EPL>((const T*)a.z + row * a.zs + t.c0, t, z);
         float n[EPL];
-        norm_n<T, EPL, MODE, WIDE>(a, t, x, z, n, red);
+        norm_n<T, E, EPL, MODE, WIDE>(a, t, x, z, n, red);
         T* y = (T*)a.y + row * a.ys + t.c0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -319,20 +329,20 @@ __global__ void __launch_bounds__(NORM_NT) k_norm_fwd(NormArgs a, int lpt) {
 
 // Partial sums of dw and db: row p of part ([np][2][C]).  Where the workgroup's teams hold
 // whole sets of groups they are added in the workgroup first, team after team (`fold`).
-template <typename T, int EPL, int MODE, bool WIDE>
+template <typename T, int E, int EPL, int MODE, bool WIDE>
 __global__ void __launch_bounds__(NORM_NT, EPL == 8 ? 4 : 2) k_norm_bwd(NormArgs a, int lpt, int fold,
                                                      float* __restrict__ part) {
-    typedef typename NormVec<T>::type vt;
-    constexpr int E = NormVec<T>::E, V = EPL / E;
+    typedef typename NormVec<T, E>::type vt;
+    constexpr int V = EPL / E;
     constexpr bool GATED = MODE >= SSD_NORM_BEFORE;
     __shared__ float red[2][NORM_NT / 64];
     extern __shared__ __align__(16) float sums[];  // fold
-    const NormTeam t0 = norm_team<T, WIDE>(a, lpt);
+    const NormTeam t0 = norm_team<T, E, WIDE>(a, lpt);
     const float inv = 1.f / (float)a.gs;
     float w[EPL], b[MODE == SSD_NORM_SILU || MODE == SSD_NORM_AFTER ? EPL : 1];
-    norm_params<T, EPL>(a.w, t0, 0.f, w);
+    norm_params<E, EPL>(a.w, t0, 0.f, w);
     if constexpr (MODE == SSD_NORM_SILU || MODE == SSD_NORM_AFTER)
-        norm_params<T, EPL>(a.b, t0, 0.f, b);
+        norm_params<E, EPL>(a.b, t0, 0.f, b);
     float sw[EPL], sb[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sw[i] = sb[i] = 0.f;
@@ -342,16 +352,16 @@ __global__ void __launch_bounds__(NORM_NT, EPL == 8 ? 4 : 2) k_norm_bwd(NormArgs
         if (WIDE && it >= a.rows * a.G) t.nv = 0;  // nothing to load or store, only to meet
         const int64_t row = WIDE && t.nv == 0 ? 0 : (uint32_t)it / (uint32_t)a.G;
         vt x[V], z[V], dy[V];
-        norm_load<T, EPL>((const T*)a.x + row * a.xs + t.c0, t, x);
-        if (GATED) norm_load<T, EPL>((const T*)a.z + row * a.zs + t.c0, t, z);
-        norm_load<T, EPL>((const T*)a.dy + row * a.ys + t.c0, t, dy);
+        norm_load<T, E, EPL>((const T*)a.x + row * a.xs + t.c0, t, x);
+        if (GATED) norm_load<T, E, EPL>((const T*)a.z + row * a.zs + t.c0, t, z);
+        norm_load<T, E, EPL>((const T*)a.dy + row * a.ys + t.c0, t, dy);
         float n[EPL], e[EPL];
-        const float r = norm_n<T, EPL, MODE, WIDE, true>(a, t, x, z, n, red);
+        const float r = norm_n<T, E, EPL, MODE, WIDE, true>(a, t, x, z, n, red);
         float s[2] = {0.f, 0.f};  // sums of g n, g
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             // vector by vector: interleaved, their temporaries do not fit the registers
-            if (i % E == 0) __builtin_amdgcn_sched_barrier(0);
+            if (i % 8 == 0) __builtin_amdgcn_sched_barrier(0);
             e[i] = (float)dy[i / E][i % E];
             if (MODE == SSD_NORM_AFTER) {
                 const float zv = (float)z[i / E][i % E];
@@ -384,7 +394,7 @@ __global__ void __launch_bounds__(NORM_NT, EPL == 8 ? 4 : 2) k_norm_bwd(NormArgs
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = t.lane + i * t.lpt;
-            __builtin_amdgcn_sched_barrier(0);
+            if (i * E % 8 == 0) __builtin_amdgcn_sched_barrier(0);
             vt ox, oz;
 #pragma unroll
             for (int j = 0; j < E; ++j) {
@@ -471,7 +481,7 @@ __global__ void __launch_bounds__(1024) k_norm_reduce(const float* __restrict__ 
 // How a problem is dealt out.
 struct NormPlan {
     bool teams, wide, fold;
-    int epl, lpt, blocks, np;
+    int e, epl, lpt, blocks, np;  // channels at a time and of a lane, lanes of a team
 };
 
 static int64_t fold_lds(const NormArgs& a, const NormPlan& p) {
@@ -487,16 +497,20 @@ static int gcd_of(int a, int b) {
     return a;
 }
 
-static NormPlan norm_plan(const NormArgs& a, int act, bool bwd, bool vectors) {
+// `e`: the channels at a time that the tensors' alignment allows
+static NormPlan norm_plan(const NormArgs& a, bool bwd, int e) {
     NormPlan p = {};
-    const int E = act == SSD_BF16 ? 8 : 4;
+    p.e = e;
     const int64_t items = a.rows * a.G;
-    // The fewest lanes that hold the group, at up to 32 channels to a lane in the forward
-    // and 16 in the backward, which has five values per channel (32 spill: 228 us for 16384
-    // rows of 2048 bf16 channels, NORM_BWD_16).
-    const int most = bwd ? 16 : 32;
-    p.teams = vectors && a.gs % E == 0 && a.gs <= most * NORM_NT;
-    p.epl = a.gs <= 8 * (bwd ? NORM_NT : 64) ? 8 : (a.gs <= 16 * 64 ? 16 : most);
+    // The fewest lanes that hold the group, at 8, 16 or 32 channels to a lane.  Forward: many,
+    // for bytes on their way and sums within a wave (16 channels of bf16 in two vectors rather
+    // than 8 in one: 36 -> 19 us for 8192 rows of 32 groups of 64); with one channel at a time 8, whose loads are as many.
+    // Backward: 8 wherever 512 lanes hold the group, since it keeps five values of each
+    // channel (16384 rows of 2048 bf16 channels: 74 us at 8, 190 at 16 and 228 at 32, which
+    // spill).
+    p.teams = a.gs <= 32 * NORM_NT;
+    if (bwd || e == 1) p.epl = a.gs <= 8 * NORM_NT ? 8 : (a.gs <= 16 * NORM_NT ? 16 : 32);
+    else p.epl = a.gs <= (e == 8 ? 8 : 8 * 64) ? 8 : (a.gs <= 16 * 64 ? 16 : 32);
     p.lpt = 1;
     while (p.lpt < NORM_NT && p.lpt * p.epl < a.gs) p.lpt *= 2;
     p.wide = p.lpt > 64;
@@ -522,47 +536,55 @@ static NormPlan norm_plan(const NormArgs& a, int act, bool bwd, bool vectors) {
     return p;
 }
 
-size_t norm_bwd_ws(const NormArgs& a, int act) {
-    // either path may run, depending on the tensors' alignment
-    const int x = norm_plan(a, act, true, false).np, y = norm_plan(a, act, true, true).np;
-    return (size_t)(x > y ? x : y) * 2 * a.C * 4;
+size_t norm_bwd_ws(const NormArgs& a, int) {
+    return (size_t)norm_plan(a, true, 1).np * 2 * a.C * 4;  // the same for every e
 }
 
-static bool norm_vectors(const NormArgs& a, int act, bool bwd) {
+static int norm_e(const NormArgs& a, int act, bool bwd) {
     const int esz = act == SSD_BF16 ? 2 : 4;
-    auto ok = [&](const void* p, int64_t stride) {
-        return p == nullptr || (((uintptr_t)p & 15) == 0 && stride * esz % 16 == 0);
+    auto fits = [&](int e) {
+        auto ok = [&](const void* p, int64_t stride) {
+            return p == nullptr || ((uintptr_t)p % (e * esz) == 0 && stride % e == 0);
+        };
+        if (a.gs % e || !ok(a.x, a.xs) || !ok(a.z, a.zs)) return false;
+        return bwd ? ok(a.dy, a.ys) && ok(a.dx, a.dxs) && ok(a.dz, a.dzs) : ok(a.y, a.ys);
     };
-    if (!ok(a.x, a.xs) || !ok(a.z, a.zs)) return false;
-    return bwd ? ok(a.dy, a.ys) && ok(a.dx, a.dxs) && ok(a.dz, a.dzs) : ok(a.y, a.ys);
+    if (fits(16 / esz)) return 16 / esz;
+    return esz == 2 && fits(2) ? 2 : 1;
 }
 
-template <typename T, int EPL, int MODE>
+template <typename T, int E, int EPL, int MODE>
 static hipError_t norm_teams(const NormArgs& a, const NormPlan& p, float* part, hipStream_t s) {
     const dim3 grid((unsigned)p.blocks), block(NORM_NT);
     if (!part) {
-        if (p.wide) return launch(k_norm_fwd<T, EPL, MODE, true>, grid, block, s, a, p.lpt);
-        return launch(k_norm_fwd<T, EPL, MODE, false>, grid, block, s, a, p.lpt);
+        if (p.wide) return launch(k_norm_fwd<T, E, EPL, MODE, true>, grid, block, s, a, p.lpt);
+        return launch(k_norm_fwd<T, E, EPL, MODE, false>, grid, block, s, a, p.lpt);
     }
-    if constexpr (EPL <= 16) {
-        const int lds = p.fold ? (int)fold_lds(a, p) : 0;
-        if (p.wide)
-            return launch_lds(k_norm_bwd<T, EPL, MODE, true>, grid, block, lds, s, a, p.lpt,
-                              (int)p.fold, part);
-        return launch_lds(k_norm_bwd<T, EPL, MODE, false>, grid, block, lds, s, a, p.lpt,
+    const int lds = p.fold ? (int)fold_lds(a, p) : 0;
+    if (p.wide)
+        return launch_lds(k_norm_bwd<T, E, EPL, MODE, true>, grid, block, lds, s, a, p.lpt,
                           (int)p.fold, part);
-    }
-    return hipErrorInvalidValue;
+    if constexpr (EPL == 8)
+        return launch_lds(k_norm_bwd<T, E, EPL, MODE, false>, grid, block, lds, s, a, p.lpt,
+                          (int)p.fold, part);
+    return hipErrorInvalidValue;  // more than 8 channels to a lane take 512 lanes
 }
 
-template <typename T, int EPL>
+template <typename T, int E, int EPL>
 static hipError_t norm_mode(const NormArgs& a, const NormPlan& p, float* part, hipStream_t s) {
     switch (a.mode) {
-        case SSD_NORM_NONE: return norm_teams<T, EPL, SSD_NORM_NONE>(a, p, part, s);
-        case SSD_NORM_SILU: return norm_teams<T, EPL, SSD_NORM_SILU>(a, p, part, s);
-        case SSD_NORM_BEFORE: return norm_teams<T, EPL, SSD_NORM_BEFORE>(a, p, part, s);
-        default: return norm_teams<T, EPL, SSD_NORM_AFTER>(a, p, part, s);
+        case SSD_NORM_NONE: return norm_teams<T, E, EPL, SSD_NORM_NONE>(a, p, part, s);
+        case SSD_NORM_SILU: return norm_teams<T, E, EPL, SSD_NORM_SILU>(a, p, part, s);
+        case SSD_NORM_BEFORE: return norm_teams<T, E, EPL, SSD_NORM_BEFORE>(a, p, part, s);
+        default: return norm_teams<T, E, EPL, SSD_NORM_AFTER>(a, p, part, s);
     }
+}
+
+template <typename T, int E>
+static hipError_t norm_epl(const NormArgs& a, const NormPlan& p, float* part, hipStream_t s) {
+    if (p.epl == 8) return norm_mode<T, E, 8>(a, p, part, s);
+    if (p.epl == 16) return norm_mode<T, E, 16>(a, p, part, s);
+    return norm_mode<T, E, 32>(a, p, part, s);
 }
 
 template <typename T>
@@ -571,18 +593,19 @@ static hipError_t norm_t(const NormArgs& a, const NormPlan& p, float* part, hipS
         if (!part) return launch(k_norm_fwd_any<T>, dim3((unsigned)p.blocks), dim3(256), s, a);
         return launch(k_norm_bwd_any<T>, dim3((unsigned)p.np, (unsigned)a.G), dim3(256), s, a, part);
     }
-    if (p.epl == 8) return norm_mode<T, 8>(a, p, part, s);
-    if (p.epl == 16) return norm_mode<T, 16>(a, p, part, s);
-    return norm_mode<T, 32>(a, p, nullptr, s);  // forward only
+    if (p.e == 1) return norm_epl<T, 1>(a, p, part, s);
+    if constexpr (sizeof(T) == 2)
+        if (p.e == 2) return norm_epl<T, 2>(a, p, part, s);
+    return norm_epl<T, 16 / (int)sizeof(T)>(a, p, part, s);
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, int act, hipStream_t s) {
-    const NormPlan p = norm_plan(a, act, false, norm_vectors(a, act, false));
+    const NormPlan p = norm_plan(a, false, norm_e(a, act, false));
     return act == SSD_BF16 ? norm_t<bf16>(a, p, nullptr, s) : norm_t<float>(a, p, nullptr, s);
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, int act, float* part, hipStream_t s) {
-    const NormPlan p = norm_plan(a, act, true, norm_vectors(a, act, true));
+    const NormPlan p = norm_plan(a, true, norm_e(a, act, true));
     SSD_TRY(act == SSD_BF16 ? norm_t<bf16>(a, p, part, s) : norm_t<float>(a, p, part, s));
     return launch(k_norm_reduce, dim3((unsigned)((2 * (int64_t)a.C + 63) / 64)), dim3(1024), s,
                   (const float*)part, p.np, a.C, a.dw, a.db);

@@ -97,7 +97,8 @@ def test_modes(mode, center, act):
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 @pytest.mark.parametrize("C,G", [(1, 1), (2, 2), (7, 1), (24, 3), (40, 5), (64, 1), (96, 2),
                                  (160, 1), (333, 3), (504, 1), (512, 8), (1000, 1), (1032, 1),
-                                 (2048, 1), (2056, 1), (4096, 2), (4104, 1), (8192, 1), (10000, 1)])
+                                 (2048, 1), (2056, 1), (4096, 2), (4104, 1), (8192, 1), (10000, 1), (84, 2),
+                                 (2004, 1), (8190, 1)])
 def test_widths(C, G, act):
     if C // G < 2:
         # a centred group of one channel has no spread: its norm is 0 and not differentiated
