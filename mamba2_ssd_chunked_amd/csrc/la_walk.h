@@ -195,8 +195,9 @@ constexpr int la_lds_bytes() {
            (OUT ? NT * (NT / LaCfg<T>::TPK) * 1024 + 16 + CD * 4 : 0);
 }
 
-// Two accumulator tiles, rounded, as one 16-byte run: a lane has channels 4 lg .. of both, and after exchanging with the lane group beside it channels 8 (lg
-// / 2) .. of the one (even groups) or the other.
+// Two accumulator tiles, rounded, as one 16-byte run: a lane has channels 4 lg .. of both, and
+// after exchanging with the lane group beside it channels 8 (lg / 2) .. of the one (even
+// groups) or the other.
 __device__ __forceinline__ bf16x8 la_pair(f32x4 a, f32x4 b) {
     typedef unsigned u2 __attribute__((ext_vector_type(2)));
     typedef unsigned u4 __attribute__((ext_vector_type(4)));
@@ -248,14 +249,16 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
     auto tokens_of = [&](int k) { return sp_.n - k * Q < Q ? sp_.n - k * Q : Q; };
     LaRows<T, BD, REV> ra, rb;
     LaRows<T, CD, REV> rc;
-    auto load = [&](int k) {
+    auto load = [&](auto& rows, const T* p, int ts, int k) {
         const int n = tokens_of(k);
-        const int64_t t0 = first_token(k, n);
-        rb.load(pb, bts, t0, n);
-        rc.load(pc, cts, t0, n);
-        if constexpr (OUT) ra.load(pa, ats, t0, n);
+        rows.load(p, ts, first_token(k, n), n);
+        __builtin_amdgcn_sched_barrier(15);  // memory accesses stay on their side
     };
-    if (nch > 0) load(0);
+    if (nch > 0) {
+        load(rb, pb, bts, 0);
+        load(rc, pc, cts, 0);
+        if constexpr (OUT) load(ra, pa, ats, 0);
+    }
 
     // the state that enters the span; this lane's elements of tile (t, u) are the four
     // channels of b from la_channel and channel 16 u + `col` of c
@@ -340,10 +343,13 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
         }
         __syncthreads();
         bool tame = false;
-        // The next chunk's rows are fetched once the scores and M a_i are done, whose
-        // registers theirs would not fit beside; the last chunk's fetch repeats it (no branch,
-        // so no full waits at a join).
-        if constexpr (!OUT) load(k + 1 < nch ? k + 1 : k);
+        // The next chunk's rows are fetched in three goes, between which the misses of the last
+        // one drain: in one go, after M a_i, the waves stand still until the CU has accepted
+        // them (the backward's walks of 2 x 8192 tokens, 32 heads of 128 x 64: 266 us instead of
+        // 280).  The last chunk's fetches repeat its rows (no branch, so no full waits at a join).
+        const int next = k + 1 < nch ? k + 1 : k;
+        load(rb, pb, bts, next);
+        if constexpr (!OUT) load(rc, pc, cts, next);
         const float keep = k + 1 == nch ? llast : (k == 0 ? lfirst : lq);
         if (OUT && n != Q) {  // the last chunk's tokens begin at row Q - n
             int i0 = lr - (Q - n) + (late && k == 0 ? 0 : 1);
@@ -363,31 +369,31 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
             for (int x = 0; x < units; ++x) {
                 const int it = first + (NT == 4 && wave == 0 ? x : 0);
                 const int kb = NT == 4 ? (wave == 0 ? 0 : (wave == 1 ? x : wave - 2)) : wave == 2;
-                Frag af[KB];
+                // both tiles' operands are read at once; a tile above the diagonal is dropped
+                Frag af[KB], bf[TPK][KB];
 #pragma unroll
-                for (int q = 0; q < KB; ++q)
+                for (int q = 0; q < KB; ++q) {
                     af[q] = M::load(sa + (16 * it + lr) * AP + KS * q + SL * lg);
+#pragma unroll
+                    for (int e = 0; e < TPK; ++e)
+                        bf[e][q] = M::load(sb + (16 * (kb * TPK + e) + lr) * AP + KS * q + SL * lg);
+                }
                 f32x4 tl[TPK];
 #pragma unroll
+                for (int e = 0; e < TPK; ++e) tl[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < KB; ++q)
+#pragma unroll
+                    for (int e = 0; e < TPK; ++e) tl[e] = M::mma(bf[e][q], af[q], tl[e]);
+#pragma unroll
                 for (int e = 0; e < TPK; ++e) {
-                    const int jt = kb * TPK + e;
-                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-                    if (jt <= it) {
+                    const int d = it - (kb * TPK + e);
+                    const float f = d <= 1 ? 1.f : (d == 2 ? l16 : l32);
 #pragma unroll
-                        for (int q = 0; q < KB; ++q)
-                            acc = M::mma(M::load(sb + (16 * jt + lr) * AP + KS * q + SL * lg),
-                                         af[q], acc);
-                        if (jt == it) {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                acc[r] = 4 * lg + r <= lr ? acc[r] * dg[r] : 0.f;
-                        } else {
-                            const float f = it - jt == 1 ? 1.f : (it - jt == 2 ? l16 : l32);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) acc[r] *= lw[r] * f;
-                        }
-                    }
-                    tl[e] = acc;
+                    for (int r = 0; r < 4; ++r)
+                        tl[e][r] = d < 0 || (d == 0 && 4 * lg + r > lr)
+                                       ? 0.f
+                                       : tl[e][r] * (d == 0 ? dg[r] : lw[r] * f);
                 }
                 sp[(it * NK + kb) * 64 + lane] = la_frag<T>(tl);
             }
@@ -406,6 +412,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
                 __syncthreads();  // before bar 2 every wave has read the flag
                 if (threadIdx.x == 0) *wild = 0;
             }
+            load(ra, pa, ats, next);
             // l^(i+1) M a_i
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -432,8 +439,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int u = 0; u < CT; ++u) o[t][u] *= row[t];
-            __builtin_amdgcn_sched_barrier(0);
-            load(k + 1 < nch ? k + 1 : k);
+            load(rc, pc, cts, next);
             __syncthreads();  // the scores are there
         }
 
@@ -444,48 +450,32 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
             for (int u = 0; u < CT; ++u)
                 cf[kb][u] = XT<T>::load(sc, CP, KS * kb, wave * CW + 16 * u, lane);
         if constexpr (OUT) {
+            Frag p[NT][NK];
 #pragma unroll
             for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
-                for (int t = kb * TPK; t < NT; ++t) {
-                    const Frag p = sp[(t * NK + kb) * 64 + lane];
+                for (int t = kb * TPK; t < NT; ++t) p[t][kb] = sp[(t * NK + kb) * 64 + lane];
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int u = 0; u < CT; ++u) o[t][u] = M::mma(cf[kb][u], p, o[t][u]);
-                }
+            for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+                for (int t = kb * TPK; t < NT; ++t)
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) o[t][u] = M::mma(cf[kb][u], p[t][kb], o[t][u]);
         }
-
-        // M <- l^n M + b^T (w c)
-#pragma unroll
-        for (int t = 0; t < BT; ++t)
-#pragma unroll
-            for (int u = 0; u < CT; ++u) St[t][u] *= keep;
-#pragma unroll
-        for (int kb = 0; kb < NK; ++kb) {
-            Frag wc[SPLITS][CT];
-#pragma unroll
-            for (int u = 0; u < CT; ++u)
-#pragma unroll
-                for (int s = 0; s < SL; ++s) {
-                    float x = (float)cf[kb][u][s] * wl * wk[kb][s];
-#pragma unroll
-                    for (int p = 0; p < SPLITS; ++p) {
-                        wc[p][u][s] = (T)x;
-                        x -= (float)wc[p][u][s];
-                    }
-                }
-#pragma unroll
-            for (int t = 0; t < BT; ++t) {
-                const Frag bt = la_bt<T>(sb, AP, KS * kb, t, lane);
-#pragma unroll
-                for (int p = SPLITS - 1; p >= 0; --p)
-#pragma unroll
-                    for (int u = 0; u < CT; ++u) St[t][u] = M::mma(bt, wc[p][u], St[t][u]);
-            }
-        }
-
         if constexpr (OUT) {
             // a lane holds channels 4 lg .. of row lr of every tile; rows without a token are
             // beyond the buffer's bound
+            if (tame)
+#pragma unroll
+                for (int u = 0; u < CT; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int first = wild_row[wave * CW + 16 * u + 4 * lg + r];
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            if (16 * t + lr >= first) o[t][u][r] = NAN;
+                    }
             typedef typename std::conditional<OUT == LA_F32, float, T>::type OT;
             const __amdgpu_buffer_rsrc_t r = buf_rsrc(
                 (OT*)w.out + first_token(k, n) * w.out_ts + (int64_t)h * CD, n * out_bytes);
@@ -511,29 +501,58 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
                         buf_store(o[t][u], r, row_at(16 * t + lr) + (wave * CW + 16 * u + 4 * lg) * 4);
             }
         }
+
+        // M <- l^n M + b^T (w c)
+#pragma unroll
+        for (int t = 0; t < BT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) St[t][u] *= keep;
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) {
+            Frag wc[SPLITS][CT];
+#pragma unroll
+            for (int u = 0; u < CT; ++u)
+#pragma unroll
+                for (int s = 0; s < SL; ++s) {
+                    float x = (float)cf[kb][u][s] * wl * wk[kb][s];
+#pragma unroll
+                    for (int p = 0; p < SPLITS; ++p) {
+                        wc[p][u][s] = (T)x;
+                        x -= (float)wc[p][u][s];
+                    }
+                }
+            // Two tiles of b are read while the products of the last two run: left to itself the
+            // compiler reads one and waits for it (span pass of 2 x 8192 tokens, 32 heads of
+            // 128 x 64: 47 us instead of 52).
+            Frag bt[2] = {la_bt<T>(sb, AP, KS * kb, 0, lane), la_bt<T>(sb, AP, KS * kb, 1, lane)};
+#pragma unroll
+            for (int t = 0; t < BT; t += 2) {
+                const int nx = t + 2 < BT ? t + 2 : t;
+                const Frag n0 = la_bt<T>(sb, AP, KS * kb, nx, lane),
+                           n1 = la_bt<T>(sb, AP, KS * kb, nx + 1, lane);
+                __builtin_amdgcn_sched_barrier(6);  // only ALU work moves across
+#pragma unroll
+                for (int p = SPLITS - 1; p >= 0; --p)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int u = 0; u < CT; ++u)
+                            St[t + e][u] = M::mma(bt[e], wc[p][u], St[t + e][u]);
+                bt[0] = n0;
+                bt[1] = n1;
+            }
+        }
+
         if (late && k == 0) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) row[t] *= l1;
         }
-        if constexpr (OUT)
-            if (tame) {
+        if (OUT && tame)
 #pragma unroll
-                for (int u = 0; u < CT; ++u)
-                    if (wild_row[col + 16 * u] < Q)
+            for (int u = 0; u < CT; ++u)
+                if (wild_row[col + 16 * u] < Q)
 #pragma unroll
-                        for (int t = 0; t < BT; ++t) St[t][u] = f32x4{NAN, NAN, NAN, NAN};
-                // over the rows that this wave has just stored
-                typedef typename std::conditional<OUT == LA_F32, float, T>::type OT;
-                __threadfence();
-#pragma unroll 1
-                for (int i = Q - n + lane; i < Q; i += 64) {
-                    const int64_t tok = first_token(k, n) + (REV ? Q - 1 - i : i - (Q - n));
-                    OT* p = (OT*)w.out + tok * w.out_ts + (int64_t)h * CD;
-#pragma unroll 1
-                    for (int c = wave * CW; c < wave * CW + CW; ++c)
-                        if (i >= wild_row[c]) p[c] = (OT)NAN;
-                }
-            }
+                    for (int t = 0; t < BT; ++t) St[t][u] = f32x4{NAN, NAN, NAN, NAN};
     }
 
     if constexpr (!OUT) {
