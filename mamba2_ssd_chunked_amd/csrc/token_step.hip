@@ -4,7 +4,9 @@
 //   S <- a S + u w^T,   o = S r      (S of [rows][cols])
 // A lane owns four neighbouring columns of some rows, a group of cols / 4 lanes a whole
 // row; the state passes through registers once per call, however many tokens it has.
-// Bound by HBM: 8 bytes per state element.
+// Bound by HBM: 8 bytes per state element (linear attention, 256 rows of 32 heads of 128 x 128:
+// 210 us, 5.1 TB/s; SSD path, 256 rows of 64 heads of 64 x 128: 214 us, 5.0 TB/s), and with one
+// row by the loads' latency (4.8 and 6.2 us).
 #include "dt_prep.h"
 #include "mixer_internal.h"
 
