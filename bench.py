@@ -88,13 +88,17 @@ CALL_KERNEL = {
 CSRC = os.path.join(ROOT, "mamba2_ssd_chunked_amd", "csrc")
 
 
+# sources of the library that no kernel of the path is built from: the peak probes and the
+# operators around the scan
+NOT_THE_PATH = ("peak_probes", "mixer_", "la_walk", "linattn", "norm", "token_step")
+
+
 def source_digest():
     """sha256 over the HIP/C++ sources: counter figures are only valid for these exact kernels."""
     import hashlib
     h = hashlib.sha256()
     for name in sorted(os.listdir(CSRC)):
-        # the peak probes are measurement kernels, not kernels of the path
-        if name.endswith((".hip", ".h", ".cpp")) and not name.startswith("peak_probes"):
+        if name.endswith((".hip", ".h", ".cpp")) and not name.startswith(NOT_THE_PATH):
             h.update(name.encode())
             with open(os.path.join(CSRC, name), "rb") as f:
                 h.update(f.read())
