@@ -47,7 +47,7 @@ extern "C" {
  * bf16 where it is a score or a state that enters an output, and taken in parts good to
  * 2^-24 (2^-17 where no state is asked for) where it enters a state.  A value of q, k, v
  * or do that is not finite reaches no other sequence and no output before it (backwards:
- * behind it); its channel's states and later outputs are then NaN. */
+ * behind it); its channel's states and later outputs are then not finite. */
 typedef struct {
     int64_t batch;      /* rows; 1 with cu_seqlens                               */
     int64_t seqlen;     /* tokens per row (with cu_seqlens: all tokens)          */

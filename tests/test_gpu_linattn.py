@@ -209,6 +209,40 @@ def test_non_finite_tokens_stay_in_their_future(bad):
     assert not torch.isfinite(got.o[:, 37]).any()
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("H,Hk", [(2, 2), (4, 2)])
+def test_a_non_finite_channel_stays_in_its_channel(H, Hk, Dk, Dv, act):
+    """One channel of v (forward) or of do (backward) that is infinite at one token: NaN in that
+    channel from that token on (backwards: up to it), every other value as without it."""
+    x = make([150, 70], H, Hk, Dk, Dv, act)
+    clean, cg = run_fwd(x), run_bwd(x)
+    at, ch, r = 83, Dv - 3, H // Hk
+    keep = x["v"][0, at, 1, ch].item()
+    x["v"][0, at, 1, ch] = float("inf")
+    got = run_fwd(x)
+    x["v"][0, at, 1, ch] = keep
+    x["do"][0, at, r, ch] = float("-inf")  # a head that reads key/value head 1
+    gg = run_bwd(x)
+    torch.cuda.synchronize()
+    hit = torch.zeros(got.o.shape, dtype=torch.bool, device="cuda")
+    hit[0, at:150, r:2 * r, ch] = True
+    assert torch.isnan(got.o[hit]).all()
+    assert torch.equal(got.o[~hit], clean.o[~hit])
+    state = torch.zeros(got.final_state.shape, dtype=torch.bool, device="cuda")
+    state[0, r:2 * r, ch] = True
+    assert torch.isnan(got.final_state[state]).all()
+    assert torch.equal(got.final_state[~state], clean.final_state[~state])
+    hit = torch.zeros(gg.dv.shape, dtype=torch.bool, device="cuda")
+    hit[0, :at + 1, 1, ch] = True
+    assert torch.isnan(gg.dv[hit]).all()
+    assert torch.equal(gg.dv[~hit], cg.dv[~hit])
+    assert torch.equal(gg.dk[:, at + 1:], cg.dk[:, at + 1:])
+    assert torch.equal(gg.dk[:, :, 0], cg.dk[:, :, 0])
+    other = [i for i in range(220) if i != at]
+    assert torch.equal(gg.dq[:, other], cg.dq[:, other])
+
+
 def test_sequences_do_not_touch_each_other():
     x = make([64, 40, 96], 2, 1, 64, 64, "bf16")
     a, ga = run_fwd(x), run_bwd(x)
@@ -393,3 +427,50 @@ def test_step_without_slots_continues_a_prompt():
     check("o", torch.cat(got, 1), whole.o[:, 80:].double().cpu(),
           A.reshape(2, 90, 4, 64)[:, 80:], t)
     check("state", state, whole.final_state.double().cpu(), Af, t)
+
+
+# ------------------------------------------------------------------- beyond 2^31 elements
+
+
+def test_tokens_far_apart():
+    """q, o, do and dq in rows that reach beyond 2^32 bytes give what packed ones give."""
+    import mamba2_ssd_chunked_amd as ssd
+    x = make([210, 90], 2, 1, 64, 128, "bf16")
+    step = (1 << 23) - 8
+
+    def far(like):
+        _, L, H, D = like.shape
+        t = torch.empty(L * step, dtype=like.dtype, device="cuda")
+        return t.as_strided(like.shape, (L * step, step, D, 1)).copy_(like)
+
+    p, want, wg = problem(x), run_fwd(x), run_bwd(x)
+    bufs = ssd.LinAttnForwardBuffers.allocate(p, 2, "cuda")
+    grads = ssd.LinAttnBackwardBuffers.allocate(p, 2, "cuda")
+    bufs.o, grads.dq = far(bufs.o), far(grads.dq)
+    x["q"] = far(x["q"])
+    run_fwd(x, bufs=bufs)
+    # do has o's stride
+    do = bufs.o
+    got = do.clone()
+    do.copy_(x["do"])
+    x["do"] = do
+    run_bwd(x, bufs=grads)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want.o)
+    for n in ("dq", "dk", "dv", "dinit"):
+        assert torch.equal(getattr(grads, n), getattr(wg, n)), n
+
+
+def test_step_in_a_large_pool():
+    """The last slot of a pool of more than 2^31 state elements gives what a small pool gives."""
+    import mamba2_ssd_chunked_amd as ssd
+    x = step_inputs(1, 2, 16, 16, 128, 128, "bf16", 1)
+    n = (1 << 31) // (16 * 128 * 128) + 2
+    pool = torch.empty(n, 16, 128, 128, dtype=torch.float32, device="cuda")
+    pool[n - 1] = x["state"][0]
+    y = [torch.empty(1, 2, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ssd.ssd_linattn_step(problem(x), x["q"], x["k"], x["v"], x["ld"], x["state"], y[0])
+    ssd.ssd_linattn_step(problem(x), x["q"], x["k"], x["v"], x["ld"], pool, y[1],
+                         slots=torch.tensor([n - 1], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(*y) and torch.equal(pool[n - 1], x["state"][0])

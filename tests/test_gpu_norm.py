@@ -187,3 +187,26 @@ def test_repeated_and_replayed_runs_are_bitwise_equal():
             assert torch.equal(getattr(b, n), getattr(g, n)), n
         run()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("C,G", [(192, 3), (21, 1), (40000, 1)])
+def test_rows_far_apart(C, G):
+    """Rows that reach beyond 2^31 elements give what packed ones give."""
+    import mamba2_ssd_chunked_amd as ssd
+    rows, step = 9, (1 << 28) - 8
+    x = make(rows, C, "before", "bf16")
+    p = ssd.make_norm(rows=rows, channels=C, ngroups=G, act="bf16", mode="before")
+    want = ssd.norm_forward(p, x["x"], x["w"], x["b"], x["z"])
+    wg = ssd.norm_backward(p, x["x"], x["w"], x["dy"], x["b"], x["z"])
+    far = lambda t: torch.empty(rows * step, dtype=t.dtype, device="cuda").as_strided(  # noqa: E731
+        t.shape, (step, 1)).copy_(t)
+    out, xx = far(torch.zeros_like(want)), far(x["x"])
+    ssd.norm_forward(p, xx, x["w"], x["b"], x["z"], out=out)
+    bufs = ssd.NormBackwardBuffers.allocate(p, "cuda")
+    bufs.dx = far(bufs.dx)
+    got = out.clone()
+    ssd.norm_backward(p, xx, x["w"], out.copy_(x["dy"]), x["b"], x["z"], bufs=bufs)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    for n in ("dx", "dz", "dweight", "dbias"):
+        assert torch.equal(getattr(bufs, n), getattr(wg, n)), n

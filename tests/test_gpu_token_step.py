@@ -210,3 +210,31 @@ def test_many_rows_equal_few(act):
         assert torch.equal(yr[0], y[r])
         for n in want:
             assert torch.equal(want[n][r], x[n][r]), (r, n)
+
+
+def test_last_slot_of_a_large_pool():
+    """States and rings of more than 2^31 elements: the last slot gives what a small pool gives."""
+    import mamba2_ssd_chunked_amd as ssd
+    H, G, P, N = 64, 1, 64, 128
+    x = draws(1, 1, H, G, P, N, 4, "bf16", 1, 4, seed=11)
+    C = x["xBC"].shape[-1]
+    n = (1 << 31) // (H * P * N) + 2
+    R = (1 << 31) // (n * C) + 2
+    state = torch.empty(n, H, P, N, dtype=torch.float32, device="cuda")
+    ring = torch.empty(n, R, C, dtype=torch.bfloat16, device="cuda")
+    state[n - 1] = x["state"][0]
+    for t in range(3, 6):  # the tokens before place 6
+        ring[n - 1, t % R] = x["conv_ring"][0, t % 4]
+    p = ssd.make_problem(batch=1, seqlen=1, nheads=H, headdim=P, dstate=N, ngroups=G, chunk=64,
+                         conv_width=4, act="bf16")
+    pos = torch.tensor([6], dtype=torch.int32, device="cuda")
+    y = [torch.empty(1, 1, H, P, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    rest = [x[k] for k in ("xBC", "conv_w", "dt_raw", "dt_bias", "A_log", "D")]
+    ssd.ssd_token_step(p, *rest, x["conv_ring"], x["state"], pos, y[0])
+    ssd.ssd_token_step(p, *rest, ring, state, pos, y[1],
+                       slots=torch.tensor([n - 1], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(*y)
+    assert torch.equal(state[n - 1], x["state"][0])
+    for t in range(3, 7):
+        assert torch.equal(ring[n - 1, t % R], x["conv_ring"][0, t % 4])
