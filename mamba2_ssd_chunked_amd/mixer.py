@@ -49,21 +49,21 @@ def _entry(fn):
 class _Args:
     """The checked tensors of one call: all of them on one device."""
 
-    __slots__ = ("act", "device")
+    __slots__ = ("act", "device", "index")
 
     def __init__(self, act):
         self.act = _TORCH_ACT[act]
-        self.device = None
+        self.device = self.index = None
 
     def _base(self, t, name, dtype, shape):
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} is required")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a device tensor")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, other tensors on {self.device}")
+        if t.get_device() != self.index:  # -1 where there is no device
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a device tensor")
+            if self.device is not None:
+                raise ValueError(f"{name} is on {t.device}, other tensors on {self.device}")
+            self.device, self.index = t.device, t.get_device()
         if t.dtype is not dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         if t.shape != shape:
@@ -105,15 +105,14 @@ class _Args:
 
     def call(self, fn, stream, *args):
         """The library call on the tensors' device; the stream comes last."""
-        dev = self.device
         if stream is None:
-            handle = torch._C._cuda_getCurrentRawStream(dev.index)
+            handle = torch._C._cuda_getCurrentRawStream(self.index)
         else:
             handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if dev.index == torch.cuda.current_device():
+        if self.index == torch._C._cuda_getDevice():
             rc = _entry(fn)(*args, handle)
         else:
-            with torch.cuda.device(dev):
+            with torch.cuda.device(self.device):
                 rc = _entry(fn)(*args, handle)
         if rc != 0:
             raise SSDError(fn, rc)
@@ -149,10 +148,12 @@ def make_linattn(*, batch: int, seqlen: int, nheads: int, keydim: int, valdim: i
                    _act_code(act), keydim ** -0.5 if scale is None else scale)
 
 
-def _strided(p: LinAttn, *strides) -> LinAttn:
+def _strided(p: LinAttn, q, k, v, o, dq=0, dk=0, dv=0) -> LinAttn:
     """The problem with the tensors' strides (a copy: the caller's stays as it is)."""
-    return LinAttn(p.batch, p.seqlen, p.nheads, p.nkvheads, p.keydim, p.valdim, p.act_dtype,
-                   p.scale, *strides)
+    c = LinAttn.from_buffer_copy(p)
+    c.q_stride, c.k_stride, c.v_stride, c.o_stride = q, k, v, o
+    c.dq_stride, c.dk_stride, c.dv_stride = dq, dk, dv
+    return c
 
 
 def _nseq(p: LinAttn, cu_seqlens) -> int:
