@@ -43,9 +43,10 @@ extern "C" {
  * values are not refused, the state then grows without bound.  The decays are
  * constants of the model: the backward gives no gradient for them.
  *
- * Sums, states and decays are float32; a bf16 product's other operand is rounded to
- * bf16 where it is a score or a state that enters an output, and taken in parts good to
- * 2^-24 (2^-17 where no state is asked for) where it enters a state.  A value of q, k, v
+ * Sums, states and decays are float32, and bf16 outputs are rounded once: where a float32
+ * value meets a bf16 one in a product it is taken in parts, good to 2^-16 (scores, states
+ * that enter an output), 2^-24 (values on their way into a state) or, where no state is
+ * asked for, 2^-17.  A value of q, k, v
  * or do that is not finite reaches no other sequence and no output before it (backwards:
  * behind it); its channel's states and later outputs are then not finite. */
 typedef struct {

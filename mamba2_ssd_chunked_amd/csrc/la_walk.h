@@ -36,10 +36,13 @@
 // 32 (t / 2) + 8 g + 4 (t % 2) + r (la_channel).  That costs nothing, since the transposed
 // reads of b address their channels in quads of any order.
 //
-// Precision.  Scores and the entering state are rounded to bf16 once as operands.  The
-// weighted c are not: a state is a float32 result, and one rounding would leave 2^-9 of it.
-// They enter as a sum of two bf16 (2^-17 of a term), of three (2^-24) where the state is
-// an output or is handed to other spans.
+// Precision.  No float32 value is rounded to bf16 as an operand, since each such rounding adds
+// 2^-9 to the one that an output has of its own (scores and entering states rounded once: root
+// mean square error 1.41 times that of the rounded exact result; quickest walks of 80 instead of
+// 87 us for 128 x 64 and of 250 instead of 287 for 128 x 128).  Scores and entering states are
+// sums of two bf16 (LaCfg::PARTS), weighted c of two (2^-17 of a term left out) where they only
+// reach bf16 outputs, and of three (float32's own rounding) in a walk whose last state is asked
+// for, in its spans' states too.
 #pragma once
 
 #include "mixer_internal.h"
@@ -51,10 +54,12 @@ template <typename T> struct LaCfg;
 template <> struct LaCfg<bf16> {
     static constexpr int Q = 64;    // tokens per chunk
     static constexpr int TPK = 2;   // 16-wide tiles per k operand
+    static constexpr int PARTS = 2; // terms of a score or an entering state as an operand
 };
 template <> struct LaCfg<float> {
     static constexpr int Q = 32;
     static constexpr int TPK = 1;
+    static constexpr int PARTS = 1;
 };
 
 // The spans of all sequences, numbered so that no scan over the lengths is needed: row s
@@ -176,16 +181,22 @@ __device__ __forceinline__ typename Mma<T>::Frag la_bt(const T* b, int pitch, in
     }
 }
 
-// A k operand from TPK stacked accumulator tiles.
+// A k operand from TPK stacked accumulator tiles, as a sum of PARTS terms: of bf16 the value cut
+// off after 8 bits and the rest of it, rounded (2^-16 of the value is left out; rounding the
+// first one as well would leave 2^-17 and makes the walks 2 % slower).
 template <typename T>
-__device__ __forceinline__ typename Mma<T>::Frag la_frag(const f32x4* tiles) {
+__device__ __forceinline__ void la_frag(const f32x4* tiles,
+                                        typename Mma<T>::Frag (&f)[LaCfg<T>::PARTS]) {
     if constexpr (sizeof(T) == 4) {
-        return tiles[0];
+        f[0] = tiles[0];
     } else {
-        typename Mma<T>::Frag f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = (bf16)tiles[e / 4][e % 4];
-        return f;
+        for (int e = 0; e < 8; ++e) {
+            const float x = tiles[e / 4][e % 4];
+            const unsigned hi = __float_as_uint(x) & 0xffff0000u;
+            f[0][e] = __builtin_bit_cast(bf16, (unsigned short)(hi >> 16));
+            f[1][e] = (bf16)(x - __uint_as_float(hi));
+        }
     }
 }
 
@@ -200,7 +211,7 @@ template <typename T, int BD, int CD, int OUT>
 constexpr int la_lds_bytes() {
     constexpr int Q = LaCfg<T>::Q, V = 16 / (int)sizeof(T), NT = Q / 16;
     return Q * (BD + V) * (int)sizeof(T) * (OUT ? 2 : 1) + Q * (CD + V) * (int)sizeof(T) +
-           (OUT ? NT * (NT / LaCfg<T>::TPK) * 1024 + 16 + CD * 4 : 0);
+           (OUT ? NT * (NT / LaCfg<T>::TPK) * LaCfg<T>::PARTS * 1024 + 16 + CD * 4 : 0);
 }
 
 // Two accumulator tiles, rounded, as one 16-byte run: a lane has channels 4 lg .. of both, and
@@ -229,14 +240,15 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
     typedef Mma<T> M;
     typedef typename M::Frag Frag;
     constexpr int Q = LaCfg<T>::Q, TPK = LaCfg<T>::TPK, NT = Q / 16, NK = NT / TPK;
+    constexpr int PARTS = LaCfg<T>::PARTS;
     constexpr int SL = M::SL, KS = M::KS, KB = BD / KS;
     constexpr int BT = BD / 16, CW = CD / 4, CT = CW / 16;  // tiles of M^T of one wave
     constexpr int AP = LaRows<T, BD, REV>::PITCH, CP = LaRows<T, CD, REV>::PITCH;
     T* sb = (T*)lds;
     T* sc = sb + Q * AP;
     T* sa = sc + Q * CP;
-    Frag* sp = (Frag*)(sa + Q * AP);  // scores, [row tile][k block][lane]
-    int* wild = (int*)(sp + NT * NK * 64);  // a c of the chunk is not finite
+    Frag* sp = (Frag*)(sa + Q * AP);  // scores, [row tile][k block][part][lane]
+    int* wild = (int*)(sp + NT * NK * PARTS * 64);  // a c of the chunk is not finite
     int* wild_row = wild + 4;               // the first such row of each channel, or Q
     if (OUT && threadIdx.x == 0) *wild = 0;
 
@@ -403,7 +415,11 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
                                        ? 0.f
                                        : tl[e][r] * (d == 0 ? dg[r] : lw[r] * f);
                 }
-                sp[(it * NK + kb) * 64 + lane] = la_frag<T>(tl);
+                Frag pf[PARTS];
+                la_frag<T>(tl, pf);
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p)
+                    sp[((it * NK + kb) * PARTS + p) * 64 + lane] = pf[p];
             }
             if (*wild) {  // for the whole workgroup
                 tame = true;
@@ -428,19 +444,21 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
                 for (int u = 0; u < CT; ++u) o[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < KB; ++q) {
-                Frag sf[CT];
+                Frag sf[CT][PARTS];
 #pragma unroll
                 for (int u = 0; u < CT; ++u) {
                     f32x4 tl[TPK];
 #pragma unroll
                     for (int e = 0; e < TPK; ++e) tl[e] = St[q * TPK + e][u];
-                    sf[u] = la_frag<T>(tl);
+                    la_frag<T>(tl, sf[u]);
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const Frag a = M::load(sa + (16 * t + lr) * AP + KS * q + SL * lg);
 #pragma unroll
-                    for (int u = 0; u < CT; ++u) o[t][u] = M::mma(sf[u], a, o[t][u]);
+                    for (int p = PARTS - 1; p >= 0; --p)
+#pragma unroll
+                        for (int u = 0; u < CT; ++u) o[t][u] = M::mma(sf[u][p], a, o[t][u]);
                 }
             }
 #pragma unroll
@@ -458,18 +476,22 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
             for (int u = 0; u < CT; ++u)
                 cf[kb][u] = XT<T>::load(sc, CP, KS * kb, wave * CW + 16 * u, lane);
         if constexpr (OUT) {
-            Frag p[NT][NK];
 #pragma unroll
-            for (int kb = 0; kb < NK; ++kb)
+            for (int part = PARTS - 1; part >= 0; --part) {
+                Frag p[NT][NK];
 #pragma unroll
-                for (int t = kb * TPK; t < NT; ++t) p[t][kb] = sp[(t * NK + kb) * 64 + lane];
-            __builtin_amdgcn_sched_barrier(0);
+                for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
-            for (int kb = 0; kb < NK; ++kb)
+                    for (int t = kb * TPK; t < NT; ++t)
+                        p[t][kb] = sp[((t * NK + kb) * PARTS + part) * 64 + lane];
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int t = kb * TPK; t < NT; ++t)
+                for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
-                    for (int u = 0; u < CT; ++u) o[t][u] = M::mma(cf[kb][u], p[t][kb], o[t][u]);
+                    for (int t = kb * TPK; t < NT; ++t)
+#pragma unroll
+                        for (int u = 0; u < CT; ++u) o[t][u] = M::mma(cf[kb][u], p[t][kb], o[t][u]);
+            }
         }
         if constexpr (OUT) {
             // a lane holds channels 4 lg .. of row lr of every tile; rows without a token are
