@@ -40,7 +40,8 @@ extern "C" {
  *                                        init, or zero
  *   o_t = scale S_t q_t
  * log_decay <= 0 is meant (minus infinity: every token sees itself alone); larger
- * values are not refused, the state then grows without bound.  The decays are
+ * values are not refused, the state then grows without bound (a power of a decay beyond
+ * float32's range counts as its largest value).  The decays are
  * constants of the model: the backward gives no gradient for them.
  *
  * Sums, states and decays are float32, and bf16 outputs are rounded once: where a float32

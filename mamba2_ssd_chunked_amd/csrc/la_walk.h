@@ -45,6 +45,8 @@
 // for, in its spans' states too.
 #pragma once
 
+#include <cfloat>
+
 #include "mixer_internal.h"
 #include "xt.h"
 
@@ -200,9 +202,17 @@ __device__ __forceinline__ void la_frag(const f32x4* tiles,
     }
 }
 
+// Decays above 1: a chunk weighs its places without a token as well, whose zeros times an
+// infinite power would be NaN.  Powers and weights are held to float32's largest value instead.
+__device__ __forceinline__ float la_held(float w) {  // 0 or above, or NaN, which it leaves
+    return w > FLT_MAX ? FLT_MAX : w;
+}
+__device__ __forceinline__ float la_within(float w) {
+    return __builtin_amdgcn_fmed3f(w, -FLT_MAX, FLT_MAX);
+}
 // l^e, the exponent's product taken in float64 so that only exp2's own ulp is left.
 __device__ __forceinline__ float la_pow(double l2, int e) {
-    return e == 0 ? 1.f : __builtin_amdgcn_exp2f((float)(l2 * (double)e));
+    return e == 0 ? 1.f : la_held(__builtin_amdgcn_exp2f((float)(l2 * (double)e)));
 }
 
 enum LaOut { LA_STATE = 0, LA_ACT = 1, LA_F32 = 2 };  // what a walk leaves behind
@@ -325,8 +335,8 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int d = lr - (4 * lg + r);
-            dg[r] = w.intra * la_pow(l2, d > 0 ? d : 0);
-            lw[r] = w.intra * la_pow(l2, 16 + d);
+            dg[r] = la_within(w.intra * la_pow(l2, d > 0 ? d : 0));
+            lw[r] = la_within(w.intra * la_pow(l2, 16 + d));
         }
     }
     // s l^(Q-1-j) of the lane's k slots, j = KS k + 16 (s / 4) + 4 lg + s % 4: a factor of
@@ -338,11 +348,11 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
 #pragma unroll
         for (int s = 0; s < SL; ++s)
             wk[k][s] = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(
-                w.state_scale * la_pow(l2, Q - 13 - (KS * k + 16 * (s / 4) + s % 4)))));
+                la_within(w.state_scale * la_pow(l2, Q - 13 - (KS * k + 16 * (s / 4) + s % 4))))));
     // The given state of a REV walk is not decayed before its first use.
     const bool late = REV && given;
     // l^n, compounded from chunk to chunk: the exact power, rounded once
-    auto power = [&](int e) { return e == 0 ? 1.f : (float)exp((double)e * (double)ld); };
+    auto power = [&](int e) { return e == 0 ? 1.f : la_held((float)exp((double)e * (double)ld)); };
     const int nlast = sp_.n - (nch - 1) * Q;
     const float lq = power(Q), lfirst = late ? power(Q - 1) : lq,
                 llast = power(late && nch == 1 ? nlast - 1 : nlast);
@@ -413,7 +423,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
                     for (int r = 0; r < 4; ++r)
                         tl[e][r] = d < 0 || (d == 0 && 4 * lg + r > lr)
                                        ? 0.f
-                                       : tl[e][r] * (d == 0 ? dg[r] : lw[r] * f);
+                                       : tl[e][r] * (d == 0 ? dg[r] : lw[r]) * f;
                 }
                 Frag pf[PARTS];
                 la_frag<T>(tl, pf);

@@ -18,7 +18,7 @@ __device__ __forceinline__ void la_compose(const LaWalk& w, const LaPlan& plan,
     const SeqRange r = seq_range(w, s);
     const int64_t n = (r.hi - r.lo + plan.span - 1) / plan.span;
     if (n < 2) return;
-    const float keep = (float)exp((double)plan.span * (double)w.log_decay[h]);
+    const float keep = la_held((float)exp((double)plan.span * (double)w.log_decay[h]));
     const int64_t step = (int64_t)w.H * quads;
     f32x4* p = ws + la_first_slot(w, plan, s) * step + (int64_t)h * quads + q;
     f32x4 m = *p;

@@ -7,6 +7,8 @@
 // Bound by HBM: 8 bytes per state element (linear attention, 256 rows of 32 heads of 128 x 128:
 // 210 us, 5.1 TB/s; SSD path, 256 rows of 64 heads of 64 x 128: 214 us, 5.0 TB/s), and with one
 // row by the loads' latency (4.8 and 6.2 us).
+#include <cfloat>
+
 #include "dt_prep.h"
 #include "mixer_internal.h"
 
@@ -46,7 +48,8 @@ __global__ void __launch_bounds__(256) k_la_step(LaStep a) {
     for (int i = 0; i < NR; ++i)
         m[i] = fresh ? f32x4{0.f, 0.f, 0.f, 0.f} : *(const f32x4*)(S + i * RPW * BD);
     if (row_taken(a.slots, a.positions, slot, row, lane)) return;
-    const float l = expf(a.log_decay[h]);
+    float l = expf(a.log_decay[h]);
+    if (l == INFINITY) l = FLT_MAX;  // a state of zeros stays one
     for (int t = 0; t < a.tokens; ++t) {
         const int64_t tok = (int64_t)row * a.tokens + t;
         const f32x4 q = load4f((const T*)a.q + tok * a.q_ts + h * BD + col);
