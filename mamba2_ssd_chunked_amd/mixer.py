@@ -353,17 +353,69 @@ class StepState:
             state=torch.empty((nslots, p.nheads, p.headdim, p.dstate), dtype=torch.float32,
                               device=device))
 
-    def load(self, problem: Problem, xBC, final_state, slots=None) -> torch.Tensor:
+    def load(self, problem: Problem, xBC, final_state, slots=None, stream=None) -> torch.Tensor:
         """Takes over rows that forward(..., want_final=True) has run, in the order of their
         tokens: the last inputs of xBC [batch, seqlen, C] and final_state [batch, H, P, N] go to
-        `slots` (distinct; rows r to slot r if None).  Returns the rows' positions."""
+        `slots` (rows r to slot r if None).  Returns the rows' positions.
+
+        As in the steps that follow, a row whose slot is outside the pool is padding and of
+        several rows with one slot only the first counts: the others go nowhere, and their
+        position is -1, so that the steps skip them too.  Work goes to the current stream, or to
+        `stream` (which waits for the current one first); give a step the same one."""
         b, L = problem.batch, problem.seqlen
-        at = torch.arange(b, device=xBC.device) if slots is None else slots.long()
-        ring = self.conv_ring.shape[1]
-        last = torch.arange(max(0, L - (problem.conv_width - 1)), L, device=xBC.device)
-        self.conv_ring[at[:, None], (last % ring)[None, :]] = xBC[:, last]
-        self.state[at] = final_state
-        return torch.full((b,), L, dtype=torch.int32, device=xBC.device)
+        n, ring, C = self.conv_ring.shape
+        if xBC.shape != (b, L, C) or xBC.dtype is not self.conv_ring.dtype:
+            raise ValueError(f"xBC must be {self.conv_ring.dtype} of shape {(b, L, C)}, got "
+                             f"{xBC.dtype} of {tuple(xBC.shape)}")
+        if final_state.shape != (b, *self.state.shape[1:]) or final_state.dtype is not torch.float32:
+            raise ValueError("final_state must be torch.float32 of shape "
+                             f"{(b, *self.state.shape[1:])}")
+        if slots is None:
+            if b > n:
+                raise ValueError(f"{b} rows need slots: the pool has {n}")
+        elif slots.shape != (b,) or slots.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"slots must be int32 or int64 of shape {(b,)}")
+        dev = self.state.device
+        positions = torch.empty((b,), dtype=torch.int32, device=dev)
+        if stream is None:
+            self._load(problem, xBC, final_state, slots, positions)
+            return positions
+        _made_for(stream, dev, positions)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        with torch.cuda.stream(stream):
+            self._load(problem, xBC, final_state, slots, positions)
+        return positions
+
+    def _load(self, problem, xBC, final_state, slots, positions):
+        b, L = problem.batch, problem.seqlen
+        n, ring, _ = self.conv_ring.shape
+        rows = torch.arange(b, device=positions.device)
+        last = torch.arange(max(0, L - (problem.conv_width - 1)), L, device=positions.device)
+        entry = (last % ring)[None, :]
+        if slots is None:
+            self.conv_ring[rows[:, None], entry] = xBC[:, last]
+            self.state[rows] = final_state
+            positions.fill_(L)
+            return
+        slots = slots.to(positions.device, torch.int64)
+        live = (slots >= 0) & (slots < n)
+        spot = torch.where(live, slots, n)
+        owner = torch.full((n + 1,), b, dtype=torch.int64, device=positions.device)
+        owner.scatter_reduce_(0, spot, rows, "amin")
+        live &= owner[spot] == rows
+        # Rows that go nowhere write the first live row's values a second time, or, if there is
+        # none, a slot's own: nothing has to come back to the host to leave them out.  (`first`
+        # of one element, since an index without dimensions is read by the host.)
+        first = live.to(torch.int32).argmax(0, keepdim=True)
+        src = torch.where(live, rows, first)
+        at = torch.where(live, slots, slots[first]).clamp(0, n - 1)
+        some = live.any()
+        ring_at = (at[:, None], entry)
+        self.conv_ring[ring_at] = torch.where(some, xBC[src[:, None], last[None, :]],
+                                              self.conv_ring[ring_at])
+        self.state[at] = torch.where(some, final_state[src], self.state[at])
+        positions.copy_(torch.where(live, L, -1))
 
 
 # ------------------------------------------- group norm with an activation, channels last
