@@ -69,7 +69,10 @@ typedef struct {
  * launch grid within the hardware's limits. */
 
 /* Bytes of workspace for the forward (SSD_WS_FORWARD) or backward (SSD_WS_BACKWARD)
- * of `nseq` sequences; 0 for an invalid problem or kind. */
+ * of `nseq` sequences (rows, or packed in one row); 0 for an invalid problem, number or
+ * kind.  It is bounded by the tokens, however many sequences they are packed into: a
+ * float32 state per head for 256 tokens or more (three in the backward), and in the
+ * backward dv and dk per head in float32 where heads share keys and values. */
 size_t ssd_linattn_workspace_bytes(const ssd_linattn* problem, int32_t nseq, int32_t kind);
 
 /* Prompts.

@@ -76,6 +76,18 @@ struct LaPlan {
 __device__ __forceinline__ int64_t la_first_slot(const LaWalk& w, const LaPlan& p, int s) {
     return w.cu ? seq_range(w, s).lo / p.span + s : (int64_t)s * p.per_row;
 }
+// Where the state that enters span j >= 1 of sequence s (first token lo) is kept; span j - 1
+// leaves there what it adds.  Packed sequences share the places of whole spans' tokens: a
+// sequence of n spans from token lo takes n - 1 of them from lo / span on, and the next one
+// begins at least (n - 1) span + 1 tokens later, so that no number of sequences needs more
+// than tokens / span.
+__device__ __forceinline__ int64_t la_place(const LaWalk& w, const LaPlan& p, int s, int64_t lo,
+                                            int64_t j) {
+    return (w.cu ? lo / p.span : (int64_t)s * (p.per_row - 1)) + j - 1;
+}
+inline int64_t la_places(const LaWalk& w, const LaPlan& p) {
+    return w.cu ? w.tokens / p.span : (int64_t)w.nseq * (p.per_row - 1);
+}
 
 struct LaSpan {
     int s, j;         // sequence, span of it; s < 0: idle
@@ -238,7 +250,7 @@ __device__ __forceinline__ bf16x8 la_pair(f32x4 a, f32x4 b) {
 }
 
 // One span of one head, by a workgroup of four waves.  SPLITS: bf16 terms per weighted c (1
-// for float32).  `ws`: the spans' states, [slot][H][wave][tile][lane] f32x4.
+// for float32).  `ws`: the states that enter spans, [place][H][wave][tile][lane] f32x4.
 //
 // A c_j that is not finite times a masked score's 0 would be NaN in the outputs before j.  A
 // chunk that has one puts 0 in its place, and NaN into the state and, from j on, the
@@ -295,7 +307,9 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
     f32x4 St[BT][CT];
     const int col = wave * CW + lr;
     const bool given = sp_.j == 0;
-    f32x4* mine = ws + ((slot * w.H + h) * 4 + wave) * (BT * CT * 64) + lane;
+    // read by a span that has one before it, written (OUT = LA_STATE) for the span behind
+    f32x4* mine = ws + ((la_place(w, plan, sp_.s, sp_.lo, sp_.j + (OUT ? 0 : 1)) * w.H + h) * 4 +
+                        wave) * (BT * CT * 64) + lane;
     const int64_t state_at = ((int64_t)sp_.s * w.H + h) * (BD * CD);
     auto at = [&](int t, int u) { return (col + 16 * u) * BD + la_channel<T>(t, lg); };
     auto at_trans = [&](int t, int u, int r) {

@@ -7,9 +7,8 @@
 
 namespace ssd {
 
-// States entering the spans of a sequence from the states its spans add: in place, slot
-// j >= 1 receives the state after span j - 1.  One lane per four state elements of a
-// (sequence, head).
+// States entering the spans of a sequence from the states its spans add, in place.  One lane per
+// four state elements of a (sequence, head).
 __device__ __forceinline__ void la_compose(const LaWalk& w, const LaPlan& plan,
                                            f32x4* __restrict__ ws, int64_t block) {
     const int quads = w.bd * w.cd / 4, per = quads / 256;
@@ -17,17 +16,15 @@ __device__ __forceinline__ void la_compose(const LaWalk& w, const LaPlan& plan,
     const int q = (int)(block % per) * 256 + threadIdx.x;
     const SeqRange r = seq_range(w, s);
     const int64_t n = (r.hi - r.lo + plan.span - 1) / plan.span;
-    if (n < 2) return;
+    if (n < 3) return;  // what the first span adds is what enters the second
     const float keep = la_held((float)exp((double)plan.span * (double)w.log_decay[h]));
     const int64_t step = (int64_t)w.H * quads;
-    f32x4* p = ws + la_first_slot(w, plan, s) * step + (int64_t)h * quads + q;
+    f32x4* p = ws + la_place(w, plan, s, r.lo, 1) * step + (int64_t)h * quads + q;
     f32x4 m = *p;
-    for (int64_t j = 1; j < n; ++j) {
+    for (int64_t j = 2; j < n; ++j) {
         p += step;
-        f32x4 add = {0.f, 0.f, 0.f, 0.f};
-        if (j + 1 < n) add = *p;
+        m = m * keep + *p;
         *p = m;
-        m = m * keep + add;
     }
 }
 __global__ void __launch_bounds__(256) k_la_spans(LaWalk w, LaPlan plan, f32x4* __restrict__ ws) {
@@ -108,7 +105,7 @@ static LaPlan la_plan(const LaWalk& w, int walks) {
 }
 
 static size_t state_ws(const LaWalk& w, const LaPlan& p) {
-    return p.split ? align256((size_t)p.slots * w.H * w.bd * w.cd * 4) : 0;
+    return p.split ? align256((size_t)la_places(w, p) * w.H * w.bd * w.cd * 4) : 0;
 }
 
 size_t la_fwd_ws(const LaWalk& w) { return state_ws(w, la_plan(w, 1)); }

@@ -1,5 +1,6 @@
 // Host side of the C ABI declared in include/ssd_mixer.h: argument validation and kernel
 // dispatch.  As in ssd_api.cpp, every check runs before anything is enqueued.
+#include <algorithm>
 #include <climits>
 #include <hip/hip_runtime.h>
 
@@ -188,12 +189,13 @@ size_t ssd_linattn_workspace_bytes(const ssd_linattn* problem, int32_t nseq, int
     if (check_linattn(problem, &st) != SSD_OK) return 0;
     if (nseq < 1 || nseq > (1 << 24) || check_walk_grid(problem, nseq) != SSD_OK) return 0;
     if (kind != SSD_WS_FORWARD && kind != SSD_WS_BACKWARD) return 0;
-    // rows or packed sequences, whichever needs more (a batch of one row may be either)
+    // rows or packed sequences, whichever needs more (one row may be either)
     const int32_t packed = 0;
-    const size_t m = linattn_ws(problem, st, nseq, nullptr, kind);
-    size_t n = problem->batch == 1 ? linattn_ws(problem, st, nseq, &packed, kind) : m;
-    if (m > n) n = m;
-    return n ? n : 256;  // 0 would say that the problem is invalid
+    if (problem->batch != 1 && nseq != problem->batch) return 0;
+    size_t n = 256;  // 0 would say that the problem is invalid
+    if (nseq == problem->batch) n = std::max(n, linattn_ws(problem, st, nseq, nullptr, kind));
+    if (problem->batch == 1) n = std::max(n, linattn_ws(problem, st, nseq, &packed, kind));
+    return n;
 }
 
 int ssd_linattn_fwd(const ssd_linattn* problem, int32_t nseq, const void* q, const void* k,
