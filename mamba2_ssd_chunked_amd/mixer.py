@@ -164,6 +164,10 @@ def _state_shape(p: LinAttn, n: int):
     return (n, p.nheads, p.valdim, p.keydim)
 
 
+def _new_states(p: LinAttn, n: int, device):
+    return torch.empty(_state_shape(p, n), dtype=torch.float32, device=device)
+
+
 def ssd_linattn_workspace_bytes(problem: LinAttn, nseq: int, kind: int = SSD_WS_FORWARD) -> int:
     return int(_entry("ssd_linattn_workspace_bytes")(ctypes.byref(problem), nseq, kind))
 
@@ -231,11 +235,12 @@ def ssd_linattn_step(problem: LinAttn, q, k, v, log_decay, state, o, slots=None,
 @dataclass
 class LinAttnForwardBuffers:
     o: torch.Tensor
-    final_state: torch.Tensor  # [nseq][H][valdim][keydim] float32
+    final_state: Optional[torch.Tensor]  # [nseq][H][valdim][keydim] float32
     ws: torch.Tensor
 
     @staticmethod
-    def allocate(problem: LinAttn, nseq: int, device) -> "LinAttnForwardBuffers":
+    def allocate(problem: LinAttn, nseq: int, device, final: bool = True) -> "LinAttnForwardBuffers":
+        """Buffers of linattn_forward; without `final` they have no final_state."""
         p = problem
         n = ssd_linattn_workspace_bytes(p, nseq, SSD_WS_FORWARD)
         if n == 0:
@@ -243,7 +248,7 @@ class LinAttnForwardBuffers:
         return LinAttnForwardBuffers(
             o=torch.empty((p.batch, p.seqlen, p.nheads, p.valdim), dtype=_TORCH_ACT[p.act_dtype],
                           device=device),
-            final_state=torch.empty(_state_shape(p, nseq), dtype=torch.float32, device=device),
+            final_state=_new_states(p, nseq, device) if final else None,
             ws=torch.empty(n, dtype=torch.uint8, device=device))
 
 
@@ -255,12 +260,15 @@ def linattn_forward(problem: LinAttn, q, k, v, log_decay, cu_seqlens=None, init=
     q [b, L, H, keydim], k and v [b, L, nkvheads, keydim or valdim]; every row is a
     sequence, or with cu_seqlens (int32 [nseq + 1], b = 1) the packed sequences are.
     init       : optional [nseq, H, valdim, keydim] float32 states before the sequences.
-    want_final : also write bufs.final_state.
+    want_final : also write bufs.final_state (None in buffers made here without it).
     Rows of bufs.o outside every sequence are left as they were.
     """
     if bufs is None:
-        bufs = LinAttnForwardBuffers.allocate(problem, _nseq(problem, cu_seqlens), q.device)
+        bufs = LinAttnForwardBuffers.allocate(problem, _nseq(problem, cu_seqlens), q.device,
+                                              final=want_final)
         _made_for(stream, q.device, bufs.o, bufs.final_state, bufs.ws)
+    elif want_final and bufs.final_state is None:
+        raise ValueError("the buffers have no final_state")
     ssd_linattn_fwd(problem, q, k, v, log_decay, cu_seqlens, init, bufs.o,
                     bufs.final_state if want_final else None, bufs.ws, stream)
     return bufs
@@ -271,11 +279,12 @@ class LinAttnBackwardBuffers:
     dq: torch.Tensor
     dk: torch.Tensor
     dv: torch.Tensor
-    dinit: torch.Tensor  # [nseq][H][valdim][keydim] float32
+    dinit: Optional[torch.Tensor]  # [nseq][H][valdim][keydim] float32
     ws: torch.Tensor
 
     @staticmethod
-    def allocate(problem: LinAttn, nseq: int, device) -> "LinAttnBackwardBuffers":
+    def allocate(problem: LinAttn, nseq: int, device, dinit: bool = True) -> "LinAttnBackwardBuffers":
+        """Buffers of linattn_backward; without `dinit` they have none."""
         p = problem
         n = ssd_linattn_workspace_bytes(p, nseq, SSD_WS_BACKWARD)
         if n == 0:
@@ -284,7 +293,7 @@ class LinAttnBackwardBuffers:
                                        device=device)
         return LinAttnBackwardBuffers(
             dq=new(p.nheads, p.keydim), dk=new(p.nkvheads, p.keydim), dv=new(p.nkvheads, p.valdim),
-            dinit=torch.empty(_state_shape(p, nseq), dtype=torch.float32, device=device),
+            dinit=_new_states(p, nseq, device) if dinit else None,
             ws=torch.empty(n, dtype=torch.uint8, device=device))
 
 
@@ -295,11 +304,15 @@ def linattn_backward(problem: LinAttn, q, k, v, log_decay, do, cu_seqlens=None, 
     buffers.  The decays are constants and get none.
 
     dfinal     : optional gradient of the final states.
-    want_dinit : also write bufs.dinit, the gradient of `init`.
+    want_dinit : also write bufs.dinit, the gradient of `init` (None in buffers made here
+                 without it).
     """
     if bufs is None:
-        bufs = LinAttnBackwardBuffers.allocate(problem, _nseq(problem, cu_seqlens), q.device)
+        bufs = LinAttnBackwardBuffers.allocate(problem, _nseq(problem, cu_seqlens), q.device,
+                                               dinit=want_dinit)
         _made_for(stream, q.device, bufs.dq, bufs.dk, bufs.dv, bufs.dinit, bufs.ws)
+    elif want_dinit and bufs.dinit is None:
+        raise ValueError("the buffers have no dinit")
     ssd_linattn_bwd(problem, q, k, v, log_decay, cu_seqlens, do, init, dfinal, bufs.dq, bufs.dk,
                     bufs.dv, bufs.dinit if want_dinit else None, bufs.ws, stream)
     return bufs

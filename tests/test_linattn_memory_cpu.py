@@ -1,6 +1,7 @@
 """How much memory the linear attention asks for (host queries, no GPU): states of spans are
 kept for a row's or a packed batch's tokens, not once more for every sequence."""
 import pytest
+import torch
 
 import mamba2_ssd_chunked_amd as ssd
 
@@ -38,3 +39,29 @@ def test_workspace_of_rows():
         # neither rows nor packed sequences
         assert ssd.ssd_linattn_workspace_bytes(p, 3, kind) == 0
         assert ssd.ssd_linattn_workspace_bytes(p, 1, kind) == 0
+
+
+def test_states_that_nobody_asked_for_are_not_made(monkeypatch):
+    from mamba2_ssd_chunked_amd import mixer
+    calls = {}
+    for n in ("ssd_linattn_fwd", "ssd_linattn_bwd"):
+        monkeypatch.setattr(mixer, n, lambda *a, n=n: calls.__setitem__(n, a))
+    p = la(64, 2, 1, 64, 64)
+    x = torch.zeros(1, 64, 2, 64)
+    f = ssd.linattn_forward(p, x, x, x, None)
+    g = ssd.linattn_backward(p, x, x, x, None, x)
+    assert f.final_state is None and g.dinit is None
+    assert calls["ssd_linattn_fwd"][8] is None and calls["ssd_linattn_bwd"][12] is None
+    f = ssd.linattn_forward(p, x, x, x, None, want_final=True)
+    g = ssd.linattn_backward(p, x, x, x, None, x, want_dinit=True)
+    assert f.final_state.shape == g.dinit.shape == (1, 2, 64, 64)
+    assert calls["ssd_linattn_fwd"][8] is f.final_state and calls["ssd_linattn_bwd"][12] is g.dinit
+    # buffers made beforehand hold both, and a call without them refuses to be asked for them
+    b = ssd.LinAttnForwardBuffers.allocate(p, 1, "cpu")
+    assert b.final_state is not None and ssd.LinAttnBackwardBuffers.allocate(p, 1, "cpu").dinit is not None
+    with pytest.raises(ValueError, match="final_state"):
+        ssd.linattn_forward(p, x, x, x, None, want_final=True,
+                            bufs=ssd.LinAttnForwardBuffers.allocate(p, 1, "cpu", final=False))
+    with pytest.raises(ValueError, match="dinit"):
+        ssd.linattn_backward(p, x, x, x, None, x, want_dinit=True,
+                             bufs=ssd.LinAttnBackwardBuffers.allocate(p, 1, "cpu", dinit=False))
