@@ -138,7 +138,8 @@ int ssd_linattn_step(const ssd_linattn* problem, const void* q, const void* k, c
  *             entries of the conv_width - 1 tokens before `positions` are read, those
  *             of the new tokens written                                     (in/out)
  *   state     [nslots][H][P][N] float32                                     (in/out)
- *   y         [batch][seqlen][H][P] act_dtype                                   (out) */
+ *   y         [batch][seqlen][H][P] act_dtype                                   (out)
+ * The state is aligned to 16 bytes, the other tensors need be to their elements only. */
 int ssd_token_step(const ssd_problem* problem, const void* xBC, const float* conv_w,
                    const void* dt_raw, const float* dt_bias, const float* A_log, const float* D,
                    const int32_t* slots, int64_t nslots, const int32_t* positions, void* conv_ring,

@@ -294,11 +294,14 @@ int ssd_token_step(const ssd_problem* p, const void* xBC, const float* conv_w, c
     if (!xBC || !conv_w || !dt_raw || !dt_bias || !A_log || !D || !positions || !conv_ring ||
         !state || !y)
         return SSD_ERR_NULL;
-    for (const void* x : {xBC, (const void*)conv_w, dt_raw, (const void*)dt_bias,
-                          (const void*)A_log, (const void*)D, (const void*)conv_ring,
-                          (const void*)state, (const void*)y})
-        if (!aligned(x, 16)) return SSD_ERR_ALIGN;
-    if (!aligned(slots, 4) || !aligned(positions, 4)) return SSD_ERR_ALIGN;
+    // all but the state is read and written element by element
+    const unsigned e = p->act_dtype == SSD_BF16 ? 2 : 4;
+    for (const void* x : {xBC, dt_raw, (const void*)conv_ring, (const void*)y})
+        if (!aligned(x, e)) return SSD_ERR_ALIGN;
+    for (const void* x : {(const void*)conv_w, (const void*)dt_bias, (const void*)A_log,
+                          (const void*)D, (const void*)slots, (const void*)positions})
+        if (!aligned(x, 4)) return SSD_ERR_ALIGN;
+    if (!aligned(state, 16)) return SSD_ERR_ALIGN;
     TokenStep a = {};
     a.xBC = xBC, a.conv_w = conv_w, a.dt_raw = dt_raw, a.dt_bias = dt_bias;
     a.A_log = A_log, a.D = D;
