@@ -41,15 +41,15 @@ extern "C" {
  *   o_t = scale S_t q_t
  * log_decay <= 0 is meant (minus infinity: every token sees itself alone); larger
  * values are not refused, the state then grows without bound (a power of a decay beyond
- * float32's range counts as its largest value).  The decays are
- * constants of the model: the backward gives no gradient for them.
+ * float32's range counts as its largest value).  The decays are constants of the model:
+ * the backward gives no gradient for them.
  *
  * Sums, states and decays are float32, and bf16 outputs are rounded once: where a float32
  * value meets a bf16 one in a product it is taken in parts, good to 2^-16 (scores, states
  * that enter an output), 2^-24 (values on their way into a state) or, where no state is
- * asked for, 2^-17.  A value of q, k, v
- * or do that is not finite reaches no other sequence and no output before it (backwards:
- * behind it); its channel's states and later outputs are then not finite. */
+ * asked for, 2^-17.  A value of q, k, v or do that is not finite reaches no other sequence
+ * and no output before it (backwards: behind it); its channel's states and later outputs
+ * are then not finite. */
 typedef struct {
     int64_t batch;      /* rows; 1 with cu_seqlens                               */
     int64_t seqlen;     /* tokens per row (with cu_seqlens: all tokens)          */

@@ -14,10 +14,12 @@
 // each span adds, a second one composes them into the states that enter the spans, and the
 // walk proper starts from those.
 //
-// What bounds it.  With a state of 128 x 64 the walk runs at 4.3 to 5.0 TB/s (2 x 8192 tokens,
-// 32 heads: 80 to 93 us), with one of 128 x 128 it issues instructions for most of its time:
-// 32768 tokens of 32 heads take 245 to 275 us, of which nine tenths are left without any memory
-// traffic, with MFMA 28 %, VALU 31 % and LDS 35 % busy at two workgroups per CU.  Chunks of 64
+// What bounds it.  With a state of 128 x 64 the walk runs at 3.8 to 4.6 TB/s (2 x 8192 tokens,
+// 32 heads: 87 to 105 us), with one of 128 x 128 it issues instructions for most of its time:
+// 32768 tokens of 32 heads take 276 to 325 us, with MFMA 33 %, VALU 34 % and LDS 31 % busy at two
+// workgroups per CU.  The figures that follow compare variants while scores and states were one
+// bf16 (walks of 80 and 250 us at the quickest, 285 on average; see Precision): without any memory
+// traffic nine tenths of the 128 x 128 walk's time were left.  Chunks of 64
 // tokens: 128 gained nothing in the pass that only forms states (110 us to 135 in the backward)
 // and double the scores' share.  Four waves: eight read each tile of LDS twice as often (338 us
 // instead of 285 for 128 x 128).
@@ -389,8 +391,8 @@ __device__ __forceinline__ void la_walk(const LaWalk& w, const LaPlan& plan,
         bool tame = false;
         // The next chunk's rows are fetched in three goes, between which the misses of the last
         // one drain: in one go, after M a_i, the waves stand still until the CU has accepted
-        // them (the backward's walks of 2 x 8192 tokens, 32 heads of 128 x 64: 266 us instead of
-        // 280).  The last chunk's fetches repeat its rows (no branch, so no full waits at a join).
+        // them (the backward's walks of 2 x 8192 tokens, 32 heads of 128 x 64, one bf16 a score:
+        // 266 us instead of 280).  The last chunk's fetches repeat its rows (no branch, so no full waits at a join).
         const int next = k + 1 < nch ? k + 1 : k;
         load(rb, pb, bts, next);
         if constexpr (!OUT) load(rc, pc, cts, next);

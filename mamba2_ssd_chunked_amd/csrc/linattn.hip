@@ -1,7 +1,7 @@
 // Linear attention with a decay per head over prompts: launches of the walk (la_walk.h),
 // the composition of span states and the sum over heads that share keys and values.
 //
-// Whole calls: 131 us forward and 333 us backward for 2 x 8192 tokens, 32 heads of 128 x 64 in
+// Whole calls: 134 us forward and 351 us backward for 2 x 8192 tokens, 32 heads of 128 x 64 in
 // bf16 (every tensor once at a copy's rate: 78 and 143 us).
 #include "la_walk.h"
 
@@ -67,14 +67,14 @@ bool la_supported(int keydim, int valdim, int act) {
 // span.  So: none up to LA_WHOLE tokens.  Longer rows are cut into the n spans that should
 // take the least time, counted in tokens that a workgroup walks one after the other: the
 // launch needs ceil(workgroups / LA_ROOM) turns of the CUs' room (two workgroups each), the
-// pass before it, over all spans but the last, 0.55 of that per token (47 against 89 us for
-// 2 x 8192 tokens, 32 heads of 128 x 64), and the rest about 256 tokens and a 64th of a span
+// pass before it, over all spans but the last, 0.55 of that per token (43 against 80 us for
+// 2 x 8192 tokens, 32 heads of 128 x 64 with scores and states of one bf16, 43 against 87 with two), and the rest about 256 tokens and a 64th of a span
 // for each.  (Three walks of those rows in 3 spans of 2731 tokens, 576 workgroups in two
 // turns: 414 us; in 8 of 1024, 1536 in three: 394 us.)  Packed sequences have their
 // lengths on the device: their tokens are cut as if into one row, but at least into two
 // turns' worth, since they fill the turns unevenly, less half a span for each sequence, whose
 // last span is as good as half empty (32768 tokens of 32 heads of 128 x 128: 415 us, without
-// that allowance 428).
+// that allowance 428; these and the 414 and 394 with one bf16).
 constexpr int LA_ROOM = 512, LA_MIN_SPAN = 256, LA_WHOLE = 1024;
 
 static LaPlan la_plan(const LaWalk& w, int walks) {

@@ -9,8 +9,8 @@
 // Bound by HBM: x, z (and dy) read once, y (dx, dz) written once.  A group of a row is held
 // in registers by a team of lanes between its statistics and its outputs; a team keeps one
 // group for all its rows, so that weight and bias, and the sums of dweight and dbias, stay
-// in registers too (16384 rows of 2048 bf16 channels, gated before: 39 us forward, 5.15 TB/s;
-// 76 us backward, 4.5 TB/s).  Groups too wide for a team take the kernels that read a group again for
+// in registers too (16384 rows of 2048 bf16 channels, gated before: 39 to 42 us forward, 4.7 to 5.1
+// TB/s; 76 us backward, 4.5 TB/s).  Groups too wide for a team take the kernels that read a group again for
 // every sweep (k_norm_*_any).
 #include "mixer_internal.h"
 
@@ -508,8 +508,9 @@ static NormPlan norm_plan(const NormArgs& a, bool bwd, int e) {
     // than 8 in one: 36 -> 19 us for 8192 rows of 32 groups of 64); with one channel at a time
     // 8, whose loads are as many.
     // Backward: 8 wherever 512 lanes hold the group, since it keeps five values of each
-    // channel (16384 rows of 2048 bf16 channels: 74 us at 8, 190 at 16 and 228 at 32, which
-    // spill).
+    // channel (16384 rows of 2048 bf16 channels: 74 us at 8, 190 at 16 and 228 at 32).  Wider groups
+    // pay for it: 151 us for 4096 channels, 289 for 5120, 783 for 10240, whose 32 channels
+    // to a lane spill.
     p.teams = a.gs <= 32 * NORM_NT;
     if (bwd || e == 1) p.epl = a.gs <= 8 * NORM_NT ? 8 : (a.gs <= 16 * NORM_NT ? 16 : 32);
     else p.epl = a.gs <= (e == 8 ? 8 : 8 * 64) ? 8 : (a.gs <= 16 * 64 ? 16 : 32);
