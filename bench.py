@@ -90,7 +90,8 @@ CSRC = os.path.join(ROOT, "mamba2_ssd_chunked_amd", "csrc")
 
 # sources of the library that no kernel of the path is built from: the peak probes and the
 # operators around the scan
-NOT_THE_PATH = ("peak_probes", "mixer_", "la_walk", "linattn", "norm", "token_step")
+NOT_THE_PATH = ("peak_probes", "mixer_", "la_walk", "linattn", "norm", "token_step", "layer_",
+                "gdelta", "block_norm", "rope")
 
 
 def source_digest():

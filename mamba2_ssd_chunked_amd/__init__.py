@@ -1,14 +1,17 @@
 """MI355X (gfx950) Mamba2 causal conv1d + SSD chunked scan with segment-local state passing.
 
-Around the scan: its single-token form, linear attention with a decay per head and the
-gated group norm of a mixer's output.
+Around the scan: its single-token form, linear attention with a decay per head, the gated
+delta rule and the gated group norm of a mixer's output.
 
 The compute path is libssd.so (hand-written HIP for CDNA4, C ABI in
-include/ssd.h and include/ssd_mixer.h).  This package only marshals torch tensors into that ABI.
+include/ssd.h, ssd_mixer.h and ssd_layer.h).  This package only marshals torch tensors into that ABI.
 """
 from ._lib import (SSD_BF16, SSD_F32, SSD_NORM_AFTER, SSD_NORM_BEFORE, SSD_NORM_NONE,
                    SSD_NORM_SILU, SSD_WS_BACKWARD, SSD_WS_FORWARD,
                    SSD_WS_FORWARD_CONV, SSDError, load)
+from .layer import (GatedDeltaBackwardBuffers, GatedDeltaForwardBuffers, gdelta_backward,
+                    gdelta_forward, make_gdelta, ssd_gdelta_bwd, ssd_gdelta_fwd, ssd_gdelta_step,
+                    ssd_gdelta_workspace_bytes)
 from .mixer import (LinAttnBackwardBuffers, LinAttnForwardBuffers, NormBackwardBuffers,
                     StepState, linattn_backward, linattn_forward, make_linattn, make_norm,
                     norm_backward, norm_forward, ssd_linattn_bwd, ssd_linattn_fwd,
@@ -28,6 +31,9 @@ __all__ = ["SSD_BF16", "SSD_F32", "SSD_NORM_AFTER", "SSD_NORM_BEFORE", "SSD_NORM
            "make_linattn", "make_norm", "norm_backward", "norm_forward", "ssd_linattn_bwd",
            "ssd_linattn_fwd", "ssd_linattn_step", "ssd_linattn_workspace_bytes", "ssd_norm_bwd",
            "ssd_norm_fwd", "ssd_norm_workspace_bytes", "ssd_token_step",
+           "GatedDeltaBackwardBuffers", "GatedDeltaForwardBuffers", "gdelta_backward",
+           "gdelta_forward", "make_gdelta", "ssd_gdelta_bwd", "ssd_gdelta_fwd", "ssd_gdelta_step",
+           "ssd_gdelta_workspace_bytes",
            "SSD_WS_BACKWARD", "SSD_WS_FORWARD", "SSD_WS_FORWARD_CONV",
            "SSDError", "load",
            "BackwardBuffers", "ForwardBuffers", "Segments", "backward", "forward",

@@ -1,4 +1,4 @@
-"""ctypes view of libssd.so (the C ABI in include/ssd.h and include/ssd_mixer.h).
+"""ctypes view of libssd.so (the C ABI in include/ssd.h, ssd_mixer.h and ssd_layer.h).
 
 Argument marshalling only: every step of the path runs in the library's HIP
 kernels.  There is no CPU fallback; if the library cannot be loaded the
@@ -56,11 +56,24 @@ class Norm(ctypes.Structure):
                 ("dz_stride", ctypes.c_int64)]
 
 
+class GatedDelta(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("nheads", ctypes.c_int32), ("nkheads", ctypes.c_int32),
+                ("keydim", ctypes.c_int32), ("valdim", ctypes.c_int32),
+                ("act_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64),
+                ("g_stride", ctypes.c_int64), ("beta_stride", ctypes.c_int64),
+                ("dq_stride", ctypes.c_int64), ("dk_stride", ctypes.c_int64),
+                ("dv_stride", ctypes.c_int64)]
+
+
 _vp = ctypes.c_void_p
 _PP = ctypes.POINTER(Problem)
 _SP = ctypes.POINTER(Segment)
 _LP = ctypes.POINTER(LinAttn)
 _NP = ctypes.POINTER(Norm)
+_GP = ctypes.POINTER(GatedDelta)
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
@@ -108,6 +121,10 @@ SIGNATURES = {
     "ssd_norm_fwd": (ctypes.c_int, [_NP] + [_vp] * 6),
     "ssd_norm_workspace_bytes": (_sz, [_NP]),
     "ssd_norm_bwd": (ctypes.c_int, [_NP] + [_vp] * 10 + [_sz, _vp]),
+    "ssd_gdelta_workspace_bytes": (_sz, [_GP, _i32, _i32]),
+    "ssd_gdelta_fwd": (ctypes.c_int, [_GP, _i32] + [_vp] * 10 + [_sz, _vp]),
+    "ssd_gdelta_bwd": (ctypes.c_int, [_GP, _i32] + [_vp] * 16 + [_sz, _vp]),
+    "ssd_gdelta_step": (ctypes.c_int, [_GP] + [_vp] * 6 + [_i64] + [_vp] * 4),
 }
 
 _lib = None

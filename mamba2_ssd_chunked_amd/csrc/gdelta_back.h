@@ -1,0 +1,578 @@
+// Backward of the gated delta rule (see gdelta.h): the walk from the last chunk to the first and the
+// chunks' gradients.
+#pragma once
+
+#include "gdelta.h"
+
+namespace ssd {
+
+template <typename T, int BD, int CT, int PT>
+constexpr int gd_back_lds() {
+    constexpr int e = sizeof(T);
+    return GD_Q * (GdRows<T, BD>::PITCH * 2 + GdRows<T, 64 * CT>::PITCH + GdMat<T, PT>::PITCH * 2) * e +
+           (int)sizeof(GdScalars) + 16;
+}
+
+// The gradient G of the state, as the forward walk keeps S: a wave owns columns of G^T.
+template <typename T, int BD, int CT, int PT>
+__global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
+    typedef Mma<T> M;
+    typedef typename M::Frag Frag;
+    constexpr int SL = M::SL, KS = M::KS, KB = BD / KS, TPK = LaCfg<T>::TPK, NK = GD_Q / KS;
+    constexpr int BT = BD / 16, CDW = 64 * CT;
+    typedef GdMat<T, PT> Mat;
+    constexpr int AP = GdRows<T, BD>::PITCH, CP = GdRows<T, CDW>::PITCH;
+    __shared__ __align__(16) unsigned char lds[gd_back_lds<T, BD, CT, PT>()];
+    T* sk = (T*)lds;
+    T* sq = sk + GD_Q * AP;
+    T* sd = sq + GD_Q * AP;
+    T* st = sd + GD_Q * CP;
+    T* sp = st + GD_Q * Mat::PITCH;
+    GdScalars* sc = (GdScalars*)(sp + GD_Q * Mat::PITCH);
+
+    const int nblk = a.valdim / CDW;
+    const GdItem it = gd_item(a, nblk);
+    if (it.s < 0) return;
+    const int h = it.h, wave = wave_id(), lane = threadIdx.x % 64, lr = lane % 16, lg = lane / 16;
+    const SeqRange sr = seq_range(a, it.s);
+    const int64_t lo = sr.lo;
+    const int len = (int)(sr.hi - sr.lo), nch = (len + GD_Q - 1) / GD_Q;
+    const int c0 = it.cb * CDW, DV = a.valdim;
+    const T* pq = (const T*)a.q + (int64_t)(h / a.share) * BD;
+    const T* pk = (const T*)a.k + (int64_t)(h / a.share) * BD;
+    const T* pd = (const T*)a.dout + (int64_t)h * DV + c0;
+    const int64_t hrow = (int64_t)h * a.tokens;
+
+    GdRows<T, BD> rk, rq;
+    GdRows<T, CDW> rd;
+    GdRows<T, Mat::D> rt, rp;
+    f32x4 rs;
+    auto tokens_of = [&](int k) { return len - k * GD_Q < GD_Q ? len - k * GD_Q : GD_Q; };
+    auto load = [&](int k) {
+        const int n = tokens_of(k);
+        const int64_t t0 = lo + (int64_t)k * GD_Q;
+        rk.load(pk, a.k_ts, t0, n);
+        rq.load(pq, a.q_ts, t0, n);
+        rd.load(pd, a.o_ts, t0, n);
+        rt.load((const T*)a.T, Mat::D, hrow + t0, n);
+        rp.load((const T*)a.P, Mat::D, hrow + t0, n);
+        rs = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (threadIdx.x < n) rs = a.sc[hrow + t0 + threadIdx.x];
+    };
+    if (nch > 0) load(nch - 1);
+
+    f32x4 G[BT][CT];
+    const int cw = wave * 16 * CT, col = c0 + cw + lr;
+    const int64_t state_at = ((int64_t)it.s * a.H + h) * ((int64_t)BD * DV);
+    auto at = [&](int t, int u) { return (col + 16 * u) * BD + la_channel<T>(t, lg); };
+#pragma unroll
+    for (int t = 0; t < BT; ++t)
+#pragma unroll
+        for (int u = 0; u < CT; ++u)
+            G[t][u] = a.dfin ? *(const f32x4*)(a.dfin + state_at + at(t, u)) : f32x4{0.f, 0.f, 0.f, 0.f};
+
+    for (int k = nch - 1; k >= 0; --k) {
+        const int n = tokens_of(k);
+        const int64_t t0 = lo + (int64_t)k * GD_Q;
+        __syncthreads();  // the last chunk's reads are done
+        rk.store(sk);
+        rq.store(sq);
+        rd.store(sd);
+        rt.store(st);
+        rp.store(sp);
+        if (wave == 0) gd_scalars_store(sc, rs);
+        __syncthreads();
+        load(k > 0 ? k - 1 : 0);
+        if (k + 1 < nch) {  // the gradient behind chunk k is kept where the state that enters k + 1 is
+            float* g = a.G + (la_place(a, plan, it.s, lo, k + 1) * a.H + h) * ((int64_t)BD * DV);
+#pragma unroll
+            for (int t = 0; t < BT; ++t)
+#pragma unroll
+                for (int u = 0; u < CT; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) g[(la_channel<T>(t, lg) + r) * DV + col + 16 * u] = G[t][u][r];
+        }
+
+        // e^(C - c) K G^T + P^T do
+        f32x4 x[GD_NT][CT];
+#pragma unroll
+        for (int t = 0; t < GD_NT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) x[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < KB; ++q) {
+            Frag gf[CT][PT];
+#pragma unroll
+            for (int u = 0; u < CT; ++u) {
+                f32x4 tl[TPK];
+#pragma unroll
+                for (int e = 0; e < TPK; ++e) tl[e] = G[q * TPK + e][u];
+                gd_split<T, PT>(tl, gf[u]);
+            }
+#pragma unroll
+            for (int t = 0; t < GD_NT; ++t) {
+                const Frag f = M::load(sk + (16 * t + lr) * AP + KS * q + SL * lg);
+#pragma unroll
+                for (int u = 0; u < CT; ++u) x[t][u] = gd_mma<T, 1, PT>(&f, gf[u], x[t][u]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < GD_NT; ++t) {
+            const f32x4 w = *(const f32x4*)(sc->out + 16 * t + 4 * lg);
+#pragma unroll
+            for (int u = 0; u < CT; ++u) x[t][u] *= w;
+        }
+        Frag df[NK][CT];
+#pragma unroll
+        for (int b = 0; b < NK; ++b)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) df[b][u] = XT<T>::load(sd, CP, KS * b, cw + 16 * u, lane);
+#pragma unroll
+        for (int b = 0; b < NK; ++b)
+#pragma unroll
+            for (int t = 0; t < (b + 1) * TPK; ++t) {
+                Frag pf[PT];
+#pragma unroll
+                for (int p = 0; p < PT; ++p) pf[p] = Mat::col(sp, t, b, p, lane);
+#pragma unroll
+                for (int u = 0; u < CT; ++u) x[t][u] = gd_mma<T, PT, 1>(pf, &df[b][u], x[t][u]);
+            }
+
+        // Z = T^T of that
+        f32x4 z[GD_NT][CT];
+#pragma unroll
+        for (int t = 0; t < GD_NT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) z[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < NK; ++b) {
+            Frag xf[CT][PT];
+#pragma unroll
+            for (int u = 0; u < CT; ++u) {
+                f32x4 tl[TPK];
+#pragma unroll
+                for (int e = 0; e < TPK; ++e) tl[e] = x[b * TPK + e][u];
+                gd_split<T, PT>(tl, xf[u]);
+            }
+#pragma unroll
+            for (int t = 0; t < (b + 1) * TPK; ++t) {
+                Frag tf[PT];
+#pragma unroll
+                for (int p = 0; p < PT; ++p) tf[p] = Mat::col(st, t, b, p, lane);
+#pragma unroll
+                for (int u = 0; u < CT; ++u) z[t][u] = gd_mma<T, PT, PT>(tf, xf[u], z[t][u]);
+            }
+        }
+        const __amdgpu_buffer_rsrc_t r = buf_rsrc(a.Z + (hrow + t0) * DV, n * DV * 4);
+#pragma unroll
+        for (int t = 0; t < GD_NT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    __builtin_amdgcn_raw_buffer_store_b32(
+                        __float_as_uint(z[t][u][q]), r, ((16 * t + 4 * lg + q) * DV + col + 16 * u) * 4, 0, 0);
+
+        // G <- e^C G + scale (e^c do)^T Q - (e^c B Z)^T K
+        const float keep = sc->in[n - 1];
+#pragma unroll
+        for (int t = 0; t < BT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) G[t][u] *= keep;
+#pragma unroll
+        for (int b = 0; b < NK; ++b) {
+            Frag wf[CT][PT], zf[CT][PT];
+#pragma unroll
+            for (int u = 0; u < CT; ++u) {
+                f32x4 tl[TPK], tz[TPK];
+#pragma unroll
+                for (int e = 0; e < TPK; ++e) {
+                    const int t = b * TPK + e;
+                    const f32x4 in = *(const f32x4*)(sc->in + 16 * t + 4 * lg);
+                    const f32x4 be = *(const f32x4*)(sc->beta + 16 * t + 4 * lg);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        tl[e][i] = a.scale * in[i] * (float)df[b][u][4 * e + i];
+                        tz[e][i] = -in[i] * be[i] * z[t][u][i];
+                    }
+                }
+                gd_split<T, PT>(tl, wf[u]);
+                gd_split<T, PT>(tz, zf[u]);
+            }
+#pragma unroll
+            for (int t = 0; t < BT; ++t) {
+                const Frag f = la_bt<T>(sq, AP, KS * b, t, lane);
+                const Frag e = la_bt<T>(sk, AP, KS * b, t, lane);
+#pragma unroll
+                for (int u = 0; u < CT; ++u) {
+                    G[t][u] = gd_mma<T, 1, PT>(&f, wf[u], G[t][u]);
+                    G[t][u] = gd_mma<T, 1, PT>(&e, zf[u], G[t][u]);
+                }
+            }
+        }
+    }
+    if (a.dinit) {
+#pragma unroll
+        for (int t = 0; t < BT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) *(f32x4*)(a.dinit + state_at + at(t, u)) = G[t][u];
+    }
+}
+
+// Parts of U, Z and E in a chunk's gradients: U and E reach dg, which is float32, Z only dk.
+template <typename T> struct GdParts { static constexpr int U = 3, Z = 2, E = 3, N = 2; };
+template <> struct GdParts<float> { static constexpr int U = 1, Z = 1, E = 1, N = 1; };
+
+template <typename T, int DK, int DV>
+struct GdChunkLds {
+    typedef GdParts<T> P;
+    static constexpr int AP = GdRows<T, DK, DK * 4>::PITCH, VP = DV + 16 / (int)sizeof(T);
+    static constexpr int EP = GdMat<T, P::E>::PITCH, NP = GdMat<T, P::N>::PITCH;
+    static constexpr bool DO = sizeof(T) == 2;  // rows of do are staged too
+    // E and N take the place of U and Z
+    static constexpr int uz = GD_Q * VP * (P::U + P::Z), en = GD_Q * (EP + NP);
+    static constexpr int rows = GD_Q * AP * 2 + (DO ? GD_Q * VP : 0) + (uz > en ? uz : en);
+    static constexpr int NW = DK / 16;
+    static constexpr int bytes = rows * (int)sizeof(T);
+};
+
+// Eight neighbouring elements as float32.
+template <typename T>
+__device__ __forceinline__ void gd_eight(const T* p, float (&v)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        const bf16x8 x = *(const bf16x8*)p;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (float)x[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[4 * e + r] = (float)p[4 * e + r];
+    }
+}
+
+// Gradients of one chunk of the heads that share a key head.  A wave owns 16 key channels: dq^T and dk^T
+// [bd][token], summed over the heads in registers, in their order.
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
+    typedef Mma<T> M;
+    typedef typename M::Frag Frag;
+    typedef GdParts<T> P;
+    typedef GdChunkLds<T, DK, DV> L;
+    typedef GdMat<T, P::E> MatE;
+    typedef GdMat<T, P::N> MatN;
+    constexpr int SL = M::SL, KS = M::KS, TPK = LaCfg<T>::TPK, NK = GD_Q / KS, KV = DV / KS;
+    constexpr int NW = L::NW, NTHR = DK * 4, AP = L::AP, VP = L::VP;
+    constexpr int TILES = NK * (NK + 1) / 2 * TPK * TPK;  // of E: whole k blocks on and below the diagonal
+    constexpr int PER = (TILES + NW - 1) / NW;
+    __shared__ __align__(16) unsigned char lds[L::bytes];
+    __shared__ double c2[GD_Q];
+    __shared__ float s_in[GD_Q], s_out[GD_Q], s_beta[GD_Q], zv[GD_Q], red[NW][GD_Q], tot[NW];
+    T* sk = (T*)lds;
+    T* sq = sk + GD_Q * AP;
+    T* sd = sq + GD_Q * AP;
+    T* su = sd + (L::DO ? GD_Q * VP : 0);
+    T* sz = su + GD_Q * VP * P::U;
+    T* se = su;
+    T* sn = se + GD_Q * L::EP;
+
+    const int groups = a.H / a.share, hk = blockIdx.x % groups;
+    const LaSpan sp = la_span(a, plan, blockIdx.x / groups);
+    if (sp.s < 0 || sp.n <= 0) return;
+    const int n = sp.n, wave = wave_id(), lane = threadIdx.x % 64, lr = lane % 16, lg = lane / 16;
+    const int64_t t0 = sp.lo + sp.i0;
+    const int b0 = 16 * wave;
+    {
+        GdRows<T, DK, NTHR> r;
+        r.load((const T*)a.k + (int64_t)hk * DK, a.k_ts, t0, n);
+        r.store(sk);
+        r.load((const T*)a.q + (int64_t)hk * DK, a.q_ts, t0, n);
+        r.store(sq);
+    }
+    f32x4 DQ[GD_NT], DKt[GD_NT];
+#pragma unroll
+    for (int t = 0; t < GD_NT; ++t) DQ[t] = DKt[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    for (int m = 0; m < a.share; ++m) {
+        const int h = hk * a.share + m;
+        const int64_t row0 = (int64_t)h * a.tokens + t0;
+        if (m > 0) __syncthreads();  // the last head's reads are done
+        if (threadIdx.x < GD_Q) {
+            const bool live = threadIdx.x < n;
+            const f32x4 s = live ? a.sc[row0 + threadIdx.x] : f32x4{0.f, 0.f, 1.f, 0.f};
+            s_in[threadIdx.x] = s[0];
+            s_out[threadIdx.x] = s[1];
+            s_beta[threadIdx.x] = s[2];
+            c2[threadIdx.x] = live ? a.c2[row0 + threadIdx.x] : -1e30;  // no factor of a row without a token
+        }
+        const T* pd = (const T*)a.dout + t0 * a.o_ts + (int64_t)h * DV;
+        if constexpr (L::DO) {
+            GdRows<T, DV, NTHR> r;
+            r.load((const T*)a.dout + (int64_t)h * DV, a.o_ts, t0, n);
+            r.store(sd);
+        }
+        // U and Z in parts; dv, dbeta and v . dv from them
+        const __amdgpu_buffer_rsrc_t ru = buf_rsrc(a.U + row0 * DV, n * DV * 4), rz = buf_rsrc(a.Z + row0 * DV, n * DV * 4);
+        constexpr int VPR = DV / 8;
+#pragma unroll
+        for (int x = threadIdx.x; x < GD_Q * VPR; x += NTHR) {
+            const int row = x / VPR, c = x % VPR * 8;
+            f32x4 u[2], z[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                u[e] = buf_load<f32x4>(ru, (row * DV + c + 4 * e) * 4);
+                z[e] = buf_load<f32x4>(rz, (row * DV + c + 4 * e) * 4);
+            }
+            const int live = row < n;
+            const float be = live ? a.sc[row0 + row][2] : 1.f;
+            float v[8], dv[8], zu = 0.f, vz = 0.f;
+            gd_eight((const T*)a.v + (t0 + (live ? row : 0)) * a.v_ts + (int64_t)h * DV + c, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                zu += z[e / 4][e % 4] * u[e / 4][e % 4];
+                dv[e] = be * z[e / 4][e % 4];
+                if (live) vz += dv[e] * v[e];
+            }
+#pragma unroll
+            for (int o = 1; o < VPR; o <<= 1) {
+                zu += __shfl_xor(zu, o, 64);
+                vz += __shfl_xor(vz, o, 64);
+            }
+            if (x % VPR == 0) zv[row] = vz;
+            if (live) {
+                if (x % VPR == 0) a.dbeta[(t0 + row) * a.H + h] = zu / be;
+                T* p = (T*)a.dv + (t0 + row) * a.dv_ts + (int64_t)h * DV + c;
+                typedef T t4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    *(t4*)(p + 4 * e) = t4{(T)dv[4 * e], (T)dv[4 * e + 1], (T)dv[4 * e + 2], (T)dv[4 * e + 3]};
+            }
+            if constexpr (sizeof(T) == 2) {
+                Frag f[P::U], g[P::Z];
+                gd_split<T, P::U>(u, f);
+                gd_split<T, P::Z>(z, g);
+#pragma unroll
+                for (int p = 0; p < P::U; ++p) *(Frag*)(su + (p * GD_Q + row) * VP + c) = f[p];
+#pragma unroll
+                for (int p = 0; p < P::Z; ++p) *(Frag*)(sz + (p * GD_Q + row) * VP + c) = g[p];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    *(f32x4*)(su + row * VP + c + 4 * e) = u[e];
+                    *(f32x4*)(sz + row * VP + c + 4 * e) = z[e];
+                }
+            }
+        }
+        __syncthreads();
+
+        // k operands of value channels: rows of do, U, Z
+        const __amdgpu_buffer_rsrc_t rdo = buf_rsrc(pd, n * (int)a.o_ts * (int)sizeof(T));
+        auto d_row = [&](int t, int q) {
+            if constexpr (L::DO) return M::load(sd + (16 * t + lr) * VP + KS * q + SL * lg);
+            else return buf_load<Frag>(rdo, ((16 * t + lr) * (int)a.o_ts + KS * q + SL * lg) * (int)sizeof(T));
+        };
+        auto u_row = [&](int t, int q, int p) { return M::load(su + (p * GD_Q + 16 * t + lr) * VP + KS * q + SL * lg); };
+        auto z_row = [&](int t, int q, int p) { return M::load(sz + (p * GD_Q + 16 * t + lr) * VP + KS * q + SL * lg); };
+
+        // tiles of E and N, transposed: a lane has row i and columns j ..
+        f32x4 E[PER], N[PER];
+        auto tile_of = [&](int y, int* ti, int* tj) {  // of whole k blocks: rows b TPK .., columns up to there
+            int b = 0, left = y;
+            while (left >= (b + 1) * TPK * TPK) left -= (b + 1) * TPK * TPK, ++b;
+            *ti = b * TPK + left / ((b + 1) * TPK);
+            *tj = left % ((b + 1) * TPK);
+        };
+#pragma unroll
+        for (int y = 0; y < PER; ++y) {
+            E[y] = N[y] = f32x4{0.f, 0.f, 0.f, 0.f};
+            const int no = y * NW + wave;
+            if (no >= TILES) continue;
+            int ti, tj;
+            tile_of(no, &ti, &tj);
+            if (tj > ti) continue;
+#pragma unroll
+            for (int q = 0; q < KV; ++q) {
+                Frag uf[P::U], zf[P::Z];
+#pragma unroll
+                for (int p = 0; p < P::U; ++p) uf[p] = u_row(tj, q, p);
+#pragma unroll
+                for (int p = 0; p < P::Z; ++p) zf[p] = z_row(ti, q, p);
+                const Frag d = d_row(ti, q);
+                E[y] = gd_mma<T, P::U, 1>(uf, &d, E[y]);
+                N[y] = gd_mma<T, P::Z, P::Z>(uf, zf, N[y]);
+            }
+            const int i = 16 * ti + lr, j = 16 * tj + 4 * lg;
+            const float bi = s_beta[i];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float f = j + r <= i ? __builtin_amdgcn_exp2f((float)(c2[i] - c2[j + r])) : 0.f;
+                E[y][r] = j + r <= i ? a.scale * f * E[y][r] : 0.f;
+                N[y][r] = j + r < i ? bi * f * N[y][r] : 0.f;
+            }
+        }
+
+        // S and G of this wave's key channels: a lane has channel b0 + lr and value channels in k order
+        f32x4 dq[GD_NT], gu[GD_NT], sz_[GD_NT];
+#pragma unroll
+        for (int t = 0; t < GD_NT; ++t) dq[t] = gu[t] = sz_[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float dot = 0.f;
+        const int64_t state = ((int64_t)sp.s * a.H + h) * ((int64_t)DK * DV);
+        const float *pS = nullptr, *pG = nullptr;  // kept ones: [bd][cd]
+        if (sp.i0 > 0) pS = a.S + (la_place(a, plan, sp.s, sp.lo, sp.j) * a.H + h) * ((int64_t)DK * DV);
+        if (!sp.last) pG = a.G + (la_place(a, plan, sp.s, sp.lo, sp.j + 1) * a.H + h) * ((int64_t)DK * DV);
+        auto channels = [&](const float* kept, const float* given, int q, f32x4 (&v)[TPK]) {
+#pragma unroll
+            for (int e = 0; e < TPK; ++e) {
+                const int c = KS * q + SL * lg + 4 * e;
+                if (kept) {
+                    v[e] = *(const f32x4*)(kept + (b0 + lr) * DV + c);
+                } else if (given) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[e][r] = given[state + (int64_t)(c + r) * DK + b0 + lr];
+                } else {
+                    v[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+            }
+        };
+#pragma unroll
+        for (int q = 0; q < KV; ++q) {
+            f32x4 s[TPK], g[TPK];
+            channels(pS, a.init, q, s);
+            channels(pG, a.dfin, q, g);
+#pragma unroll
+            for (int e = 0; e < TPK; ++e)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dot += s[e][r] * g[e][r];
+            Frag sf[P::U], gf[P::U];
+            gd_split<T, P::U>(s, sf);
+            gd_split<T, P::U>(g, gf);
+#pragma unroll
+            for (int t = 0; t < GD_NT; ++t) {
+                Frag uf[P::U], zf[P::Z];
+#pragma unroll
+                for (int p = 0; p < P::U; ++p) uf[p] = u_row(t, q, p);
+#pragma unroll
+                for (int p = 0; p < P::Z; ++p) zf[p] = z_row(t, q, p);
+                const Frag d = d_row(t, q);
+                dq[t] = gd_mma<T, P::U, 1>(sf, &d, dq[t]);
+                gu[t] = gd_mma<T, P::U, P::U>(gf, uf, gu[t]);
+                sz_[t] = gd_mma<T, P::Z, P::Z>(sf, zf, sz_[t]);
+            }
+        }
+        // <G, S behind> = e^C <G, S> + sum_j e^(C - c_j) k_j . (G u_j)
+        dot *= s_in[n - 1];
+        typedef T t4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int t = 0; t < GD_NT; ++t) {
+            const int i = 16 * t + lr;
+            const t4 kv = *(const t4*)(sk + i * AP + b0 + 4 * lg);
+            const float in = s_in[i], be = s_beta[i];
+            gu[t] *= s_out[i];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dot += (float)kv[r] * gu[t][r];
+            dq[t] *= a.scale * in;
+            gu[t] -= sz_[t] * (in * be);
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) dot += __shfl_xor(dot, o, 64);
+        if (lane == 0) tot[wave] = dot;
+        __syncthreads();  // U and Z are read
+#pragma unroll
+        for (int y = 0; y < PER; ++y) {
+            const int no = y * NW + wave;
+            if (no >= TILES) continue;
+            int ti, tj;
+            tile_of(no, &ti, &tj);
+            T* pe = se + (16 * ti + lr) * L::EP + MatE::at(tj, lg);
+            T* pn = sn + (16 * ti + lr) * L::NP + MatN::at(tj, lg);
+            if constexpr (sizeof(T) == 2) {
+                f32x4 two[2] = {E[y], N[y]};
+                Frag f[P::E];
+                gd_split<T, P::E>(two, f);  // the first four of a part are E's
+#pragma unroll
+                for (int p = 0; p < P::E; ++p) {
+                    *(bf16x4*)(pe + p * GD_Q) = __builtin_shufflevector(f[p], f[p], 0, 1, 2, 3);
+                    if (p < P::N) *(bf16x4*)(pn + p * GD_Q) = __builtin_shufflevector(f[p], f[p], 4, 5, 6, 7);
+                }
+            } else {
+                *(f32x4*)pe = E[y];
+                *(f32x4*)pn = N[y];
+            }
+        }
+        __syncthreads();
+        // dq += E K; dk += E^T Q - (N + N^T) K
+#pragma unroll
+        for (int b = 0; b < NK; ++b) {
+            const Frag kf = XT<T>::load(sk, AP, KS * b, b0, lane), qf = XT<T>::load(sq, AP, KS * b, b0, lane);
+            Frag nk = kf;
+#pragma unroll
+            for (int s = 0; s < SL; ++s) nk[s] = -kf[s];
+#pragma unroll
+            for (int t = b * TPK; t < GD_NT; ++t) {
+                Frag ef[P::E], nf[P::N];
+#pragma unroll
+                for (int p = 0; p < P::E; ++p) ef[p] = MatE::row(se, t, b, p, lane);
+#pragma unroll
+                for (int p = 0; p < P::N; ++p) nf[p] = MatN::row(sn, t, b, p, lane);
+                dq[t] = gd_mma<T, 1, P::E>(&kf, ef, dq[t]);
+                gu[t] = gd_mma<T, 1, P::N>(&nk, nf, gu[t]);
+            }
+#pragma unroll
+            for (int t = 0; t < (b + 1) * TPK; ++t) {
+                Frag ef[P::N], nf[P::N];
+#pragma unroll
+                for (int p = 0; p < P::N; ++p) {
+                    ef[p] = MatE::col(se, t, b, p, lane);
+                    nf[p] = MatN::col(sn, t, b, p, lane);
+                }
+                gu[t] = gd_mma<T, 1, P::N>(&qf, ef, gu[t]);
+                gu[t] = gd_mma<T, 1, P::N>(&nk, nf, gu[t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < GD_NT; ++t) {
+            const t4 qv = *(const t4*)(sq + (16 * t + lr) * AP + b0 + 4 * lg);
+            float d = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d += (float)qv[r] * dq[t][r];
+            d += __shfl_xor(d, 16, 64);
+            d += __shfl_xor(d, 32, 64);
+            if (lg == 0) red[wave][16 * t + lr] = d;
+            DQ[t] += dq[t];
+            DKt[t] += gu[t];
+        }
+        __syncthreads();
+        if (wave == 0) {  // dg_t: the sum from t on
+            double d = -(double)zv[lane], all = 0.0;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                d += (double)red[w][lane];
+                all += (double)tot[w];
+            }
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const double down = __shfl_down(d, o, 64);
+                if (lane + o < 64) d += down;
+            }
+            if (lane < n) a.dg[(t0 + lane) * a.H + h] = (float)(d + all);
+        }
+    }
+
+    auto write = [&](const f32x4 (&v)[GD_NT], void* out, int64_t ts) {
+        const int bytes = (int)ts * (int)sizeof(T);
+        const __amdgpu_buffer_rsrc_t r = buf_rsrc((T*)out + t0 * ts + (int64_t)hk * DK, n * bytes);
+        if constexpr (sizeof(T) == 2) {
+            const int half = lg & 1, c8 = b0 + 8 * (lg >> 1);
+#pragma unroll
+            for (int t = 0; t < GD_NT; t += 2)
+                buf_store(la_pair(v[t], v[t + 1]), r, (16 * (t + half) + lr) * bytes + c8 * 2);
+        } else {
+#pragma unroll
+            for (int t = 0; t < GD_NT; ++t) buf_store(v[t], r, (16 * t + lr) * bytes + (b0 + 4 * lg) * 4);
+        }
+    };
+    write(DQ, a.dq, a.dq_ts);
+    write(DKt, a.dk, a.dk_ts);
+}
+
+}  // namespace ssd

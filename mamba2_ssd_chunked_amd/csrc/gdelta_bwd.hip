@@ -1,0 +1,57 @@
+// Backward of the gated delta rule over prompts: launches of gdelta_prep.h, gdelta_walk.h and
+// gdelta_back.h.
+#include "gdelta_back.h"
+#include "gdelta_prep.h"
+#include "gdelta_walk.h"
+
+namespace ssd {
+
+// T and P in three parts, per-token factors, U and Z, entering states and leaving gradients.
+struct GdBwdWs {
+    size_t T, P, sc, c2, U, Z, S, G, total;
+};
+static GdBwdWs bwd_layout(const GdArgs& a, int act) {
+    const size_t rows = (size_t)a.H * a.tokens, mat = rows * GD_Q * (act == SSD_BF16 ? 6 : 4);
+    const size_t states = (size_t)la_places(a, gd_plan(a)) * a.H * a.keydim * a.valdim * 4;
+    GdBwdWs w;
+    w.T = 0;
+    w.P = align256(w.T + mat);
+    w.sc = align256(w.P + mat);
+    w.c2 = align256(w.sc + rows * sizeof(f32x4));
+    w.U = align256(w.c2 + rows * sizeof(double));
+    w.Z = align256(w.U + rows * a.valdim * 4);
+    w.S = align256(w.Z + rows * a.valdim * 4);
+    w.G = align256(w.S + states);
+    w.total = align256(w.G + states);
+    return w;
+}
+size_t gd_bwd_ws(const GdArgs& a, int act) { return bwd_layout(a, act).total; }
+
+template <typename T, int DK, int DV>
+static hipError_t bwd_dims(const GdArgs& a, hipStream_t s) {
+    constexpr int PT = sizeof(T) == 2 ? 3 : 1, CT = 1;
+    const LaPlan p = gd_plan(a);
+    const dim3 walk = gd_grid(a, DV / (64 * CT));
+    SSD_TRY(launch(k_gd_prep<T, DK, PT, PT, false>, dim3((unsigned)(p.slots * a.H)), dim3(256), s, a, p));
+    SSD_TRY(launch(k_gd_walk<T, DK, CT, PT, true>, walk, dim3(256), s, a, p));
+    SSD_TRY(launch(k_gd_back<T, DK, CT, PT>, walk, dim3(256), s, a, p));
+    return launch(k_gd_chunk<T, DK, DV>, dim3((unsigned)(p.slots * (a.H / a.share))), dim3(DK * 4), s, a, p);
+}
+
+template <typename T>
+static hipError_t bwd_t(const GdArgs& a, hipStream_t s) {
+    if (a.keydim == 64) return a.valdim == 64 ? bwd_dims<T, 64, 64>(a, s) : bwd_dims<T, 64, 128>(a, s);
+    return a.valdim == 64 ? bwd_dims<T, 128, 64>(a, s) : bwd_dims<T, 128, 128>(a, s);
+}
+
+hipError_t launch_gd_bwd(GdArgs a, int act, void* ws, hipStream_t s) {
+    const GdBwdWs w = bwd_layout(a, act);
+    char* p = (char*)ws;
+    a.T = p + w.T, a.P = p + w.P;
+    a.sc = (f32x4*)(p + w.sc), a.c2 = (double*)(p + w.c2);
+    a.U = (float*)(p + w.U), a.Z = (float*)(p + w.Z);
+    a.S = (float*)(p + w.S), a.G = (float*)(p + w.G);
+    return act == SSD_BF16 ? bwd_t<bf16>(a, s) : bwd_t<float>(a, s);
+}
+
+}  // namespace ssd

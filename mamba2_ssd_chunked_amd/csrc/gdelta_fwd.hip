@@ -1,0 +1,49 @@
+// The gated delta rule over prompts, forward: launches of gdelta_prep.h and gdelta_walk.h.
+#include "gdelta_prep.h"
+#include "gdelta_walk.h"
+
+namespace ssd {
+
+// T in three parts (two without a last state), P in two, per-token factors.
+struct GdFwdWs {
+    size_t T, P, sc, total;
+};
+static GdFwdWs fwd_layout(const GdArgs& a, int act) {
+    const size_t rows = (size_t)a.H * a.tokens, e = act == SSD_BF16 ? 2 : 4;
+    GdFwdWs w;
+    w.T = 0;
+    w.P = align256(w.T + rows * GD_Q * (act == SSD_BF16 ? 3 : 1) * e);
+    w.sc = align256(w.P + rows * GD_Q * (act == SSD_BF16 ? 2 : 1) * e);
+    w.total = align256(w.sc + rows * sizeof(f32x4));
+    return w;
+}
+size_t gd_fwd_ws(const GdArgs& a, int act) { return fwd_layout(a, act).total; }
+
+template <typename T, int DK, int CT, int PT>
+static hipError_t fwd_parts(const GdArgs& a, hipStream_t s) {
+    constexpr int PO = sizeof(T) == 2 ? 2 : 1;
+    const LaPlan p = gd_plan(a);
+    SSD_TRY(launch(k_gd_prep<T, DK, PT, PO, true>, dim3((unsigned)(p.slots * a.H)), dim3(256), s, a, p));
+    return launch(k_gd_walk<T, DK, CT, PT, false>, gd_grid(a, a.valdim / (64 * CT)), dim3(256), s, a, p);
+}
+
+template <typename T, int DK>
+static hipError_t fwd_dk(const GdArgs& a, hipStream_t s) {
+    if constexpr (sizeof(T) == 4) return fwd_parts<T, DK, 1, 1>(a, s);
+    else return a.fin ? fwd_parts<T, DK, 1, 3>(a, s) : fwd_parts<T, DK, 1, 2>(a, s);
+}
+
+template <typename T>
+static hipError_t fwd_t(const GdArgs& a, hipStream_t s) {
+    return a.keydim == 64 ? fwd_dk<T, 64>(a, s) : fwd_dk<T, 128>(a, s);
+}
+
+hipError_t launch_gd_fwd(GdArgs a, int act, void* ws, hipStream_t s) {
+    const GdFwdWs w = fwd_layout(a, act);
+    a.T = (char*)ws + w.T;
+    a.P = (char*)ws + w.P;
+    a.sc = (f32x4*)((char*)ws + w.sc);
+    return act == SSD_BF16 ? fwd_t<bf16>(a, s) : fwd_t<float>(a, s);
+}
+
+}  // namespace ssd

@@ -75,7 +75,8 @@ struct LaPlan {
     int64_t slots;  // numbers handed out
     bool split;     // some sequence may have more than one span
 };
-__device__ __forceinline__ int64_t la_first_slot(const LaWalk& w, const LaPlan& p, int s) {
+template <typename W>
+__device__ __forceinline__ int64_t la_first_slot(const W& w, const LaPlan& p, int s) {
     return w.cu ? seq_range(w, s).lo / p.span + s : (int64_t)s * p.per_row;
 }
 // Where the state that enters span j >= 1 of sequence s (first token lo) is kept; span j - 1
@@ -83,11 +84,13 @@ __device__ __forceinline__ int64_t la_first_slot(const LaWalk& w, const LaPlan& 
 // sequence of n spans from token lo takes n - 1 of them from lo / span on, and the next one
 // begins at least (n - 1) span + 1 tokens later, so that no number of sequences needs more
 // than tokens / span.
-__device__ __forceinline__ int64_t la_place(const LaWalk& w, const LaPlan& p, int s, int64_t lo,
+template <typename W>
+__device__ __forceinline__ int64_t la_place(const W& w, const LaPlan& p, int s, int64_t lo,
                                             int64_t j) {
     return (w.cu ? lo / p.span : (int64_t)s * (p.per_row - 1)) + j - 1;
 }
-inline int64_t la_places(const LaWalk& w, const LaPlan& p) {
+template <typename W>
+inline int64_t la_places(const W& w, const LaPlan& p) {
     return w.cu ? w.tokens / p.span : (int64_t)w.nseq * (p.per_row - 1);
 }
 
@@ -98,7 +101,8 @@ struct LaSpan {
     bool last;
 };
 
-__device__ __forceinline__ LaSpan la_span(const LaWalk& w, const LaPlan& p, int64_t slot) {
+template <typename W>
+__device__ __forceinline__ LaSpan la_span(const W& w, const LaPlan& p, int64_t slot) {
     int a = 0, b = w.nseq - 1;  // the last sequence whose numbers start at or below slot
     if (!w.cu) a = b = (int)(slot / p.per_row);
     while (a < b) {

@@ -48,11 +48,13 @@ struct LaWalk {
 };
 
 // Sequence s as token range [lo, hi) over all rows; offsets outside the tokens are cut
-// off, so that no table makes a kernel leave its tensors.
+// off, so that no table makes a kernel leave its tensors.  W: a problem with `cu`, `seqlen` and
+// `tokens`.
 struct SeqRange {
     int64_t lo, hi;
 };
-__device__ __forceinline__ SeqRange seq_range(const LaWalk& w, int s) {
+template <typename W>
+__device__ __forceinline__ SeqRange seq_range(const W& w, int s) {
     SeqRange r;
     if (w.cu) {
         const int64_t a = w.cu[s], b = w.cu[s + 1];
