@@ -4,6 +4,8 @@
  *
  *   ssd_gdelta_*    the gated delta rule: a state with a decay and an update rate per token and
  *                   head; prompts (forward and backward) and single tokens.
+ *   ssd_block_norm_* the norms before and after a block, with its gate and residual scale.
+ *   ssd_rope        rotary positions of queries and keys, and their gradient.
  */
 #ifndef MI355X_SSD_LAYER_H
 #define MI355X_SSD_LAYER_H
@@ -98,6 +100,91 @@ int ssd_gdelta_bwd(const ssd_gdelta* problem, int32_t nseq, const void* q, const
 int ssd_gdelta_step(const ssd_gdelta* problem, const void* q, const void* k, const void* v,
                     const float* g, const float* beta, const int32_t* slots, int64_t nslots,
                     const int32_t* positions, float* state, void* o, void* stream);
+
+/* ---- norms around a block ---------------------------------------------------------
+ *
+ * Per row (token) of `channels`, with norm(u) = (u - m) / sqrt(mean((u - m)^2) + eps), m = mean(u)
+ * if `center`, else 0; x the residual stream and y what the block gives:
+ *   u = norm(y) post_weight + post_bias      (post; else y)
+ *   m = u act(z)                             (a gate; else u)
+ *   r = alpha x + scale m                    the residual stream behind the block
+ *   h = norm(r) pre_weight + pre_bias        (pre) what the next block reads
+ * All in float32; r and h are rounded once, and h is made of r before its rounding. */
+typedef enum {
+    SSD_GATE_NONE = 0,
+    SSD_GATE_LINEAR = 1,   /* act(z) = z          */
+    SSD_GATE_SIGMOID = 2,
+    SSD_GATE_SILU = 3
+} ssd_gate;
+typedef struct {
+    int64_t rows;
+    int32_t channels;   /* up to 16384 (SSD_ERR_UNSUPPORTED beyond)               */
+    int32_t act_dtype;  /* ssd_dtype of y, z, h and their gradients              */
+    int32_t res_dtype;  /* ssd_dtype of x, r and their gradients: act_dtype's, or SSD_F32 */
+    int32_t post, pre;  /* 0 or 1: the two norms                                 */
+    int32_t gate;       /* ssd_gate                                              */
+    int32_t center;     /* 0 or 1, of both norms                                 */
+    float alpha, eps;   /* eps > 0                                               */
+    /* elements between rows, 0 = packed; any value >= channels below 2^28, and tensors need be
+     * aligned to their elements only.  r_stride is that of r and of dr, h_stride of h and dh. */
+    int64_t x_stride, y_stride, z_stride, r_stride, h_stride, dx_stride, dy_stride, dz_stride;
+} ssd_block;
+/* Size limit (SSD_ERR_SHAPE beyond it): rows <= 2^31 - 1. */
+
+/* x [rows][channels] res_dtype, y and z (a gate only) act_dtype, scale [channels] float32 or NULL (one),
+ * post_weight and pre_weight [channels] float32 (their norms only), post_bias and pre_bias likewise or
+ * NULL -> r, and h with `pre`.  r may be x itself, h may be y or z itself. */
+int ssd_block_norm_fwd(const ssd_block* problem, const void* x, const void* y, const void* z,
+                       const float* scale, const float* post_weight, const float* post_bias,
+                       const float* pre_weight, const float* pre_bias, void* r, void* h, void* stream);
+
+/* Bytes of workspace of ssd_block_norm_bwd; 0 for an invalid problem. */
+size_t ssd_block_norm_workspace_bytes(const ssd_block* problem);
+
+/* Gradients, with dr of r (NULL: zero; only with `pre`) and dh of h (with `pre`).  dx, dy and dz (a gate
+ * only) [rows][channels]; dscale, dpost_*, dpre_* [channels] float32, summed over the rows; each of
+ * these may be NULL.  dx may be x or dr itself, dy may be y or dh, dz may be z. */
+int ssd_block_norm_bwd(const ssd_block* problem, const void* x, const void* y, const void* z,
+                       const float* scale, const float* post_weight, const float* post_bias,
+                       const float* pre_weight, const void* dr, const void* dh, void* dx, void* dy,
+                       void* dz, float* dscale, float* dpost_weight, float* dpost_bias,
+                       float* dpre_weight, float* dpre_bias, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- rotary positions --------------------------------------------------------------
+ *
+ * The first `rotdim` channels of every head are taken as rotdim / 2 pairs, pair i is turned by the
+ * angle p frequencies[i] at position p and multiplied by `factor`; the others are copied:
+ *   y1 = factor (x1 cos - x2 sin),  y2 = factor (x2 cos + x1 sin)
+ * Pairs are channels (i, i + rotdim / 2) (SSD_ROPE_HALF) or (2 i, 2 i + 1) (SSD_ROPE_INTERLEAVED).
+ * Frequencies that stretch a model to longer contexts are the caller's to choose; angles are formed
+ * in float64, so that far positions lose nothing. */
+typedef enum { SSD_ROPE_HALF = 0, SSD_ROPE_INTERLEAVED = 1 } ssd_rope_style;
+typedef struct {
+    int64_t batch, seqlen;
+    int32_t nheads, nkheads;  /* heads of q and of k; 0 of k: none                */
+    int32_t headdim;          /* up to 1024 (SSD_ERR_UNSUPPORTED beyond)          */
+    int32_t rotdim;           /* even, 2 .. headdim                               */
+    int32_t act_dtype;        /* ssd_dtype of all                                 */
+    int32_t style;            /* ssd_rope_style                                   */
+    float factor;
+    /* elements between tokens, 0 = packed, below 2^28; the tensors need be aligned to their
+     * elements only */
+    int64_t q_stride, k_stride, qo_stride, ko_stride;
+} ssd_rope_problem;
+/* Size limits (SSD_ERR_SHAPE beyond them): batch * seqlen <= 2^31 - 128 tokens, heads <= 65535. */
+
+/*   q [batch][seqlen][nheads][headdim], k [batch][seqlen][nkheads][headdim] (in)
+ *   frequencies [rotdim / 2] float64, radians per position                  (in)
+ *   positions  [batch][seqlen] int32, of any sign, or NULL: a token's place in its row, or in its
+ *              sequence where cu_seqlens is given                           (in)
+ *   cu_seqlens [nseq + 1] int32 or NULL, as for ssd_linattn_fwd: tokens outside every
+ *              sequence are left as they were                               (in)
+ *   inverse    0, or 1: turned back by the same angles (and multiplied by `factor`), which takes
+ *              gradients of the outputs to those of the inputs
+ *   q_out, k_out as q, k; they may be q and k themselves                    (out) */
+int ssd_rope(const ssd_rope_problem* problem, const void* q, const void* k, const double* frequencies,
+             const int32_t* positions, const int32_t* cu_seqlens, int32_t nseq, int32_t inverse,
+             void* q_out, void* k_out, void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,8 @@ SSD_WS_FORWARD = 0
 SSD_WS_BACKWARD = 1
 SSD_WS_FORWARD_CONV = 2
 SSD_NORM_NONE, SSD_NORM_SILU, SSD_NORM_BEFORE, SSD_NORM_AFTER = range(4)
+SSD_GATE_NONE, SSD_GATE_LINEAR, SSD_GATE_SIGMOID, SSD_GATE_SILU = range(4)
+SSD_ROPE_HALF, SSD_ROPE_INTERLEAVED = range(2)
 SSD_MAX_SEGMENTS = 64
 SSD_SCRATCH_BYTES = 64 << 20
 
@@ -68,12 +70,35 @@ class GatedDelta(ctypes.Structure):
                 ("dv_stride", ctypes.c_int64)]
 
 
+class BlockNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int32),
+                ("act_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
+                ("post", ctypes.c_int32), ("pre", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("center", ctypes.c_int32), ("alpha", ctypes.c_float), ("eps", ctypes.c_float),
+                ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("z_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64),
+                ("h_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+                ("dy_stride", ctypes.c_int64), ("dz_stride", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("nheads", ctypes.c_int32), ("nkheads", ctypes.c_int32),
+                ("headdim", ctypes.c_int32), ("rotdim", ctypes.c_int32),
+                ("act_dtype", ctypes.c_int32), ("style", ctypes.c_int32),
+                ("factor", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("qo_stride", ctypes.c_int64), ("ko_stride", ctypes.c_int64)]
+
+
 _vp = ctypes.c_void_p
 _PP = ctypes.POINTER(Problem)
 _SP = ctypes.POINTER(Segment)
 _LP = ctypes.POINTER(LinAttn)
 _NP = ctypes.POINTER(Norm)
 _GP = ctypes.POINTER(GatedDelta)
+_BP = ctypes.POINTER(BlockNorm)
+_RP = ctypes.POINTER(Rope)
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
@@ -125,6 +150,10 @@ SIGNATURES = {
     "ssd_gdelta_fwd": (ctypes.c_int, [_GP, _i32] + [_vp] * 10 + [_sz, _vp]),
     "ssd_gdelta_bwd": (ctypes.c_int, [_GP, _i32] + [_vp] * 16 + [_sz, _vp]),
     "ssd_gdelta_step": (ctypes.c_int, [_GP] + [_vp] * 6 + [_i64] + [_vp] * 4),
+    "ssd_block_norm_fwd": (ctypes.c_int, [_BP] + [_vp] * 11),
+    "ssd_block_norm_workspace_bytes": (_sz, [_BP]),
+    "ssd_block_norm_bwd": (ctypes.c_int, [_BP] + [_vp] * 18 + [_sz, _vp]),
+    "ssd_rope": (ctypes.c_int, [_RP] + [_vp] * 5 + [_i32] * 2 + [_vp] * 3),
 }
 
 _lib = None

@@ -22,7 +22,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["ssd_api.cpp", "conv1d.hip", "ssd_fwd.hip", "scan.hip", "ssd_bwd.hip", "noalloc.hip",
            "mixer_api.cpp", "linattn.hip", "token_step.hip", "norm.hip", "layer_api.cpp",
-           "gdelta_fwd.hip", "gdelta_bwd.hip", "gdelta_step.hip"]
+           "gdelta_fwd.hip", "gdelta_bwd.hip", "gdelta_step.hip", "block_norm.hip",
+           "rope.hip"]
 PROBE_SOURCES = ["peak_probes.hip"]
 # The probes' MFMA loops keep their accumulators in ordinary VGPRs, updated in
 # place: with accumulation registers the allocator copies every chain's

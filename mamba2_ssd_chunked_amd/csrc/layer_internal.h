@@ -52,4 +52,34 @@ struct GdStep {
 };
 hipError_t launch_gd_step(const GdStep& a, int act, hipStream_t s);
 
+// ---- norms around a block ------------------------------------------------------------
+struct BlockArgs {
+    const void *x, *y, *z, *dr, *dh;
+    const float *scale, *w1, *b1, *w2, *b2;  // 1: of the norm behind the block, 2: before the next
+    void *r, *h, *dx, *dy, *dz;
+    float *dscale, *dw1, *db1, *dw2, *db2;
+    int64_t rows, xs, ys, zs, rs, hs, dxs, dys, dzs;
+    int C, post, pre, gate, center;
+    float alpha, eps;
+};
+constexpr int BLOCK_MAX_CHANNELS = 16384;
+size_t block_bwd_ws(const BlockArgs& a);
+hipError_t launch_block_fwd(const BlockArgs& a, int act, int res, hipStream_t s);
+hipError_t launch_block_bwd(const BlockArgs& a, int act, int res, float* part, hipStream_t s);
+
+// ---- rotary positions ------------------------------------------------------------------
+struct RopeArgs {
+    const void *q, *k;
+    void *qo, *ko;
+    int64_t qs, ks, qos, kos;
+    const double* freq;
+    const int32_t *positions, *cu;
+    int nseq;
+    int64_t seqlen, tokens;
+    int H, K, D, R, style;
+    float factor, turn;  // turn: 1 or -1
+};
+constexpr int ROPE_MAX_DIM = 1024;
+hipError_t launch_rope(const RopeArgs& a, int act, hipStream_t s);
+
 }  // namespace ssd

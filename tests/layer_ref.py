@@ -75,3 +75,40 @@ def gdelta_bwd(q, k, v, g, beta, scale, sequences, do, init=None, dfinal=None):
     for name in ("dq", "dk"):
         out[name] = out[name].reshape(T, Hk, r, Dk).sum(2)
     return out
+
+
+def _norm(u, w, b, center, eps):
+    m = u.mean(-1, keepdim=True) if center else 0.0
+    n = (u - m) / torch.sqrt(((u - m) ** 2).mean(-1, keepdim=True) + eps)
+    return n * w + (0.0 if b is None else b)
+
+
+def act(kind, z):
+    return {"linear": z, "sigmoid": 1 / (1 + torch.exp(-z)), "silu": z / (1 + torch.exp(-z))}[kind]
+
+
+def block_norm(t, *, gate, center, alpha, eps):
+    """(r, h) of float64 tensors t: x, y and what there is of z, scale, post_weight, post_bias,
+    pre_weight, pre_bias."""
+    u = t["y"]
+    if t.get("post_weight") is not None:
+        u = _norm(u, t["post_weight"], t.get("post_bias"), center, eps)
+    if gate != "none":
+        u = u * act(gate, t["z"])
+    r = alpha * t["x"] + (1.0 if t.get("scale") is None else t["scale"]) * u
+    if t.get("pre_weight") is None:
+        return r, None
+    return r, _norm(r, t["pre_weight"], t.get("pre_bias"), center, eps)
+
+
+def rope(x, angles, factor, rotdim, style, inverse):
+    """x [..., heads, dim] float64 turned by angles [..., rotdim / 2]."""
+    y = x.clone()
+    a, b = ((slice(0, rotdim // 2), slice(rotdim // 2, rotdim)) if style == "half"
+            else (slice(0, rotdim, 2), slice(1, rotdim, 2)))
+    c, s = torch.cos(angles)[..., None, :] * factor, torch.sin(angles)[..., None, :] * factor
+    if inverse:
+        s = -s
+    y[..., a] = x[..., a] * c - x[..., b] * s
+    y[..., b] = x[..., b] * c + x[..., a] * s
+    return y

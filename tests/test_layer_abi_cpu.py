@@ -114,3 +114,110 @@ def test_tensors_on_the_host_are_refused():
     q, v, g = torch.zeros(1, 3, 2, 128, dtype=torch.bfloat16), torch.zeros(1, 3, 8, 64, dtype=torch.bfloat16), torch.zeros(1, 3, 8)
     with pytest.raises(ValueError, match="device tensor"):
         ssd.gdelta_forward(p, q, q, v, g, g)
+
+
+def block(rows=8, channels=512, act="bf16", res="f32", gate="silu", **kw):
+    strides = {k: kw.pop(k) for k in list(kw) if k.endswith("_stride")}
+    fields = {k: kw.pop(k) for k in list(kw) if k in ("post_", "center_")}
+    p = ssd.make_block_norm(rows=rows, channels=channels, act=act, res=res, gate=gate, **kw)
+    for k, v in strides.items():
+        setattr(p, k, v)
+    for k, v in fields.items():
+        setattr(p, k[:-1], v)
+    return p
+
+
+def block_fwd(p, **kw):
+    t = dict(x=FAKE, y=FAKE, z=FAKE, scale=FAKE, pw=FAKE, pb=FAKE, w=FAKE, b=FAKE, r=FAKE, h=FAKE)
+    t.update(kw)
+    return _lib.load().ssd_block_norm_fwd(ref(p), *[t[n] for n in ("x", "y", "z", "scale", "pw", "pb", "w", "b", "r", "h")],
+                                          None)
+
+
+def block_bwd(p, ws=FAKE, n=BIG, **kw):
+    names = ("x", "y", "z", "scale", "pw", "pb", "w", "dr", "dh", "dx", "dy", "dz", "ds", "dpw", "dpb", "dw", "db")
+    t = dict.fromkeys(names, FAKE)
+    t.update(kw)
+    return _lib.load().ssd_block_norm_bwd(ref(p), *[t[n_] for n_ in names], ws, n, None)
+
+
+def test_other_struct_layouts():
+    assert ctypes.sizeof(_lib.BlockNorm) == 112 and ctypes.sizeof(_lib.Rope) == 80
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), -2), (dict(rows=1 << 31), -2), (dict(channels=0), -2), (dict(channels=16385), -3),
+    (dict(act=2), -3), (dict(act="f32", res="bf16"), -3), (dict(gate=4), -3), (dict(post_=2), -2),
+    (dict(center_=-1), -2), (dict(eps=0.0), -2), (dict(eps=float("nan")), -2), (dict(x_stride=511), -2),
+    (dict(dz_stride=1 << 28), -2),
+])
+def test_block_norm_problem(kw, code):
+    p = block(**kw)
+    assert block_fwd(p) == code and block_bwd(p) == code
+    assert ssd.ssd_block_norm_workspace_bytes(p) == 0
+
+
+def test_block_norm_pointers():
+    p = block()
+    assert block_fwd(None) == -1 and block_bwd(None) == -1
+    for name in ("x", "y", "z", "pw", "w", "r", "h"):
+        assert block_fwd(p, **{name: None}) == -1
+    for name in ("x", "y", "z", "pw", "w", "dh", "dx", "dy", "dz"):
+        assert block_bwd(p, **{name: None}) == -1
+    assert block_bwd(block(pre=False), dr=None) == -1
+    for name in ("x", "r", "scale", "b"):
+        assert block_fwd(p, **{name: FAKE + 2}) == -4
+    for name in ("y", "z", "h"):
+        assert block_fwd(p, **{name: FAKE + 1}) == -4
+    assert block_bwd(p, dr=FAKE + 2) == -4 and block_bwd(p, dpw=FAKE + 1) == -4
+    need = ssd.ssd_block_norm_workspace_bytes(p)
+    assert need > 0 and block_bwd(p, n=need - 1) == -5 and block_bwd(p, ws=None) == -5
+
+
+def rope(**kw):
+    base = dict(batch=2, seqlen=9, nheads=4, nkheads=2, headdim=64, rotdim=32, act="bf16")
+    strides = {k: kw.pop(k) for k in list(kw) if k.endswith("_stride")}
+    p = ssd.make_rope(**dict(base, **kw))
+    for k, v in strides.items():
+        setattr(p, k, v)
+    return p
+
+
+def rope_call(p, nseq=0, inverse=0, **kw):
+    t = dict(q=FAKE, k=FAKE, f=FAKE, pos=None, cu=None, qo=FAKE, ko=FAKE)
+    t.update(kw)
+    return _lib.load().ssd_rope(ref(p), t["q"], t["k"], t["f"], t["pos"], t["cu"], nseq, inverse, t["qo"], t["ko"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), -2), (dict(seqlen=0), -2), (dict(nheads=0), -2), (dict(nkheads=-1), -2),
+    (dict(nheads=65536), -2), (dict(headdim=1025), -3), (dict(rotdim=31), -2), (dict(rotdim=66), -2),
+    (dict(rotdim=0), -2), (dict(act=2), -3), (dict(style=2), -3), (dict(seqlen=1 << 31), -2),
+    (dict(q_stride=255), -2), (dict(ko_stride=1 << 28), -2),
+])
+def test_rope_problem(kw, code):
+    assert rope_call(rope(**kw)) == code
+
+
+def test_rope_pointers():
+    p = rope()
+    assert rope_call(None) == -1
+    for name in ("q", "k", "f", "qo", "ko"):
+        assert rope_call(p, **{name: None}) == -1
+    assert rope_call(p, inverse=2) == -2
+    assert rope_call(p, cu=FAKE, nseq=2) == -7 and rope_call(rope(batch=1), cu=FAKE, nseq=0) == -7
+    assert rope_call(p, q=FAKE + 1) == -4 and rope_call(p, f=FAKE + 4) == -4 and rope_call(p, pos=FAKE + 2) == -4
+
+
+def test_frequencies():
+    f, m = ssd.rope_frequencies(8, base=16.0)
+    assert torch.allclose(f, torch.tensor([1.0, 0.5, 0.25, 0.125]).double()) and m == 1.0
+    assert torch.allclose(ssd.rope_frequencies(8, scaling="linear", stretch=4.0)[0] * 4, ssd.rope_frequencies(8)[0])
+    plain, ntk = ssd.rope_frequencies(64)[0], ssd.rope_frequencies(64, scaling="ntk", stretch=8.0)[0]
+    assert ntk[0] == plain[0] and abs(float(ntk[-1] * 8 / plain[-1]) - 1) < 1e-12
+    f, m = ssd.rope_frequencies(128, scaling="yarn", stretch=16.0)
+    plain = ssd.rope_frequencies(128)[0]
+    assert torch.equal(f[:20], plain[:20]) and torch.allclose(f[50:] * 16, plain[50:]) and 1.27 < m < 1.28
+    for bad in (dict(rotdim=7), dict(rotdim=8, scaling="other"), dict(rotdim=8, stretch=0.5)):
+        with pytest.raises(ValueError):
+            ssd.rope_frequencies(**bad)

@@ -44,3 +44,23 @@ def test_gdelta_backward_against_differences():
         want = float((got["d" + name] * d).sum())
         # central differences: h^2 of a third derivative, and 2^-52 / h of the values
         assert abs(step - want) < 1e-7 * max(1.0, abs(want)), name
+
+
+def test_block_norm_of_one_row():
+    x, y = torch.tensor([[1.0, -2.0, 3.0]]).double(), torch.tensor([[3.0, 0.0, -4.0]]).double()
+    one = torch.ones(3).double()
+    r, h = R.block_norm(dict(x=x, y=y, z=2 * one[None], scale=0.5 * one, post_weight=one, pre_weight=2 * one),
+                        gate="linear", center=False, alpha=2.0, eps=0.0)
+    n = (25 / 3) ** 0.5
+    want = 2 * x + torch.tensor([[3.0, 0.0, -4.0]]).double() / n
+    assert torch.allclose(r, want) and torch.allclose(h, 2 * want / want.square().mean().sqrt())
+
+
+def test_rope_turns_pairs():
+    x = torch.tensor([[[1.0, 2.0, 3.0, 4.0, 9.0]]]).double()
+    quarter = torch.tensor([[torch.pi / 2, torch.pi]]).double()
+    half = R.rope(x, quarter, 2.0, 4, "half", False)
+    assert torch.allclose(half, torch.tensor([[[-6.0, -4.0, 2.0, -8.0, 9.0]]]).double())
+    inter = R.rope(x, quarter, 1.0, 4, "interleaved", False)
+    assert torch.allclose(inter, torch.tensor([[[-2.0, 1.0, -3.0, -4.0, 9.0]]]).double())
+    assert torch.allclose(R.rope(inter, quarter, 1.0, 4, "interleaved", True), x)
