@@ -29,7 +29,9 @@ PROBE_SOURCES = ["peak_probes.hip"]
 # place: with accumulation registers the allocator copies every chain's
 # accumulator between registers each round, and the copies wait for the
 # products.  (The SSD kernels get the in-place VGPR form without the flag.)
-EXTRA_FLAGS = {"peak_probes.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# The gated delta rule's kernels have more registers than one wave's VGPRs at hand and would get the copies too.
+_VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+EXTRA_FLAGS = {name: _VGPR_FORM for name in ("peak_probes.hip", "gdelta_fwd.hip", "gdelta_bwd.hip")}
 
 FLAGS = [f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -40,28 +40,44 @@ namespace ssd {
 
 constexpr int GD_Q = GD_CHUNK, GD_NT = GD_Q / 16;
 
-// Parts of a float32 value as an operand: bf16 cut off after 8 bits each, the last one rounded.
-// Two leave out 2^-16 of it, three 2^-24.
+// Parts of a float32 value as an operand: bf16 rounded, and so the remainders, which are exact.  Two
+// leave out 2^-18 of it, three nothing.  The remainder of a value of a pair is one dot product, of the pair's
+// bf16 and (-1, 0) or (0, -1), where taking the part apart and subtracting it would be two
+// instructions.  (The constants come from registers: as immediates the compiler encodes (-1, 0) as what the
+// hardware reads as (0, -1).)
 template <typename T, int P>
 __device__ __forceinline__ void gd_split(const f32x4* tiles, typename Mma<T>::Frag (&f)[P]) {
     if constexpr (sizeof(T) == 4) {
         f[0] = tiles[0];
     } else {
+        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+        unsigned first = 0x0000bf80u, second = 0xbf800000u;
+        asm("" : "+s"(first), "+s"(second));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float x = tiles[e / 4][e % 4];
+        for (int e = 0; e < 8; e += 2) {
+            float x = tiles[e / 4][e % 4], y = tiles[e / 4][e % 4 + 1];
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                if (p == P - 1) {
-                    f[p][e] = (bf16)x;
-                } else {
-                    const unsigned hi = __float_as_uint(x) & 0xffff0000u;
-                    f[p][e] = __builtin_bit_cast(bf16, (unsigned short)(hi >> 16));
-                    x -= __uint_as_float(hi);
+                const b2 h = {(bf16)x, (bf16)y};
+                f[p][e] = h[0];
+                f[p][e + 1] = h[1];
+                if (p < P - 1) {
+                    x = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(b2, first), x, false);
+                    y = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(b2, second), y, false);
                 }
             }
         }
     }
+}
+
+// f(0), f(1), .. f(N - 1) with constants.
+template <int... I, typename F>
+__device__ __forceinline__ void gd_each(std::integer_sequence<int, I...>, F&& f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void gd_for(F&& f) {
+    gd_each(std::make_integer_sequence<int, N>{}, f);
 }
 
 // Rows of D elements of a chunk on their way into LDS, by NTHR threads; rows without a token are
@@ -100,10 +116,143 @@ struct GdRows {
     }
 };
 
-// A row of T or P: for each part 64 columns, in the order of an operand's k slots: column 32 b + 16 e
-// + 4 g + r stands at 32 b + 8 g + 4 e + r (float32: as it is).
+// ---- staging -----------------------------------------------------------------------------------
+// A chunk's operands go from memory to LDS without passing through registers (buffer_load ... lds: lane l of
+// a wave writes 16 bytes at the wave's address + 16 l; beyond the bound it writes zeros), while the chunk
+// before is computed: two buffers, one barrier per chunk.  The compiler does not know of these loads:
+// gd_wait is what waits for them.
+typedef int gd_i4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ gd_i4 gd_rsrc(const void* p, int bytes) {
+    const uint64_t a = (uint64_t)p;
+    return gd_i4{__builtin_amdgcn_readfirstlane((int)a), __builtin_amdgcn_readfirstlane((int)(a >> 32) & 0xffff),
+                 __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
+}
+__device__ __forceinline__ unsigned gd_lds(const void* p) {
+    return __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
+}
+__device__ __forceinline__ void gd_dma16(gd_i4 r, unsigned lds, int off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
+                 : "memory");
+}
+__device__ __forceinline__ void gd_dma4(gd_i4 r, unsigned lds, int off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
+                 : "memory");
+}
+// Until at most N of this wave's memory accesses are on their way: all but the last N are done.
+template <int N>
+__device__ __forceinline__ void gd_wait() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// 64 rows of D elements in LDS, without padding: the 16-byte pieces of a row are exchanged by its number,
+// so that neither 16 rows' pieces nor the transposed reads of 4-row groups meet in a bank (of the
+// latter half of each piece is read at once: twice is the least).
+template <typename T, int D>
+struct GdTile {
+    static constexpr int RB = D * (int)sizeof(T), PPR = RB / 16, BYTES = GD_Q * RB;
+    __device__ static __forceinline__ int flip(int row) {
+        if constexpr (sizeof(T) == 4) return (4 * ((row >> 2) & 3)) ^ (row & 3);
+        else if constexpr (D == 128) return (4 * (row & 3)) ^ (2 * ((row >> 2) & 1));
+        else return (4 * ((row >> 1) & 1)) ^ (2 * ((row >> 2) & 1));
+    }
+    __device__ static __forceinline__ int at(int row, int piece) { return row * RB + ((piece ^ flip(row)) << 4); }
+    static constexpr int FETCHES = BYTES / 4096;  // of each of four waves
+    // the j-th fetch of a wave of rows `bytes` apart
+    __device__ static __forceinline__ void fetch(gd_i4 r, int bytes, unsigned lds, int j, int wave, int lane) {
+        const int i = 4 * j + wave, x = i * 64 + lane, row = x / PPR, piece = (x % PPR) ^ flip(row);
+        gd_dma16(r, lds + i * 1024, row * bytes + piece * 16);
+    }
+    // row operand: rows of tile t, k block q
+    __device__ static __forceinline__ typename Mma<T>::Frag row(const char* m, int t, int q, int lane) {
+        const int lr = lane % 16, lg = lane / 16;
+        return *(const typename Mma<T>::Frag*)(m + 16 * t * RB + at(lr, 4 * q + lg));
+    }
+    // transposed, k the tokens from jb: columns of tile t in the order of la_channel ...
+    __device__ static __forceinline__ typename Mma<T>::Frag bt(const char* m, int jb, int t, int lane) {
+        if constexpr (sizeof(T) == 4) return xt(m, jb, 16 * t, lane);
+        else return tr(m, jb, lane, 4 * (t / 2) + lane % 4, 8 * (t % 2));
+    }
+    // ... or the 16 from p0 on
+    __device__ static __forceinline__ typename Mma<T>::Frag xt(const char* m, int jb, int p0, int lane) {
+        if constexpr (sizeof(T) == 4) {
+            const int i = lane % 16, g = lane / 16;
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = *(const float*)(m + jb * RB + at(4 * g + e, p0 / 4 + i / 4) + 4 * (i % 4));
+            return v;
+        } else {
+            return tr(m, jb, lane, p0 / 8 + (lane % 4) / 2, 8 * (lane % 2));
+        }
+    }
+    __device__ static __forceinline__ bf16x8 tr(const char* m, int jb, int lane, int piece, int byte) {
+        typedef short s4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s4 lds_s4;
+        const char* a = m + jb * RB + at(4 * (lane / 16) + lane % 16 / 4, piece) + byte;
+        const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)a));
+        const bf16x4 hi = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(a + 16 * RB)));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+// T or P.  In memory a row per token: for each part 64 columns, in the order of an operand's k slots (column
+// 32 b + 16 e + 4 g + r stands at 32 b + 8 g + 4 e + r; float32: as it is).  In LDS the operands
+// one after the other, those on and below the diagonal: 64 lanes' 16 bytes, a lane group's rows
+// exchanged by its number against bank conflicts of the transposed reads.
 template <typename T, int PARTS>
 struct GdMat {
+    typedef typename Mma<T>::Frag Frag;
+    static constexpr int TPK = LaCfg<T>::TPK, NK = GD_Q / Mma<T>::KS;
+    static constexpr int D = GD_Q * PARTS, NTB = NK * (NK + 1) / 2 * TPK, BYTES = NTB * PARTS * 1024;
+    __device__ static __forceinline__ int tb(int t, int b) {  // of (row tile, k block)
+        return TPK == 2 ? (t < 2 ? t : 2 * t - 2 + b) : t * (t + 1) / 2 + b;
+    }
+    __device__ static __forceinline__ int slot(int lg, int lr) { return 16 * lg + (lr ^ (4 * lg)); }
+    static constexpr int FETCHES = (NTB * PARTS + 3) / 4;  // of each of four waves
+    static constexpr int ROW = D * (int)sizeof(T);         // bytes of a row in memory
+    __device__ static __forceinline__ void fetch(gd_i4 r, unsigned lds, int j, int wave, int lane) {
+        const int k = 4 * j + wave, i = k < NTB * PARTS ? k : NTB * PARTS - 1, x = i / PARTS, p = i % PARTS;
+        int t, b;
+        if constexpr (TPK == 2) {
+            t = x < 2 ? x : x / 2 + 1;
+            b = x < 2 ? 0 : x % 2;
+        } else {
+            t = x < 1 ? 0 : (x < 3 ? 1 : (x < 6 ? 2 : 3));
+            b = x - t * (t + 1) / 2;
+        }
+        const int lg = lane / 16, row = 16 * t + ((lane % 16) ^ (4 * lg));
+        gd_dma16(r, lds + i * 1024, row * ROW + 16 * lg + p * (GD_Q * (int)sizeof(T)) + 64 * b);
+    }
+    // row operand of tile t, columns of k block b
+    __device__ static __forceinline__ Frag row(const char* m, int t, int b, int part, int lane) {
+        return *(const Frag*)(m + (tb(t, b) * PARTS + part) * 1024 + slot(lane / 16, lane % 16) * 16);
+    }
+    // the transposed matrix's: rows are columns of tile t, k the rows of block b
+    __device__ static __forceinline__ Frag col(const char* m, int t, int b, int part, int lane) {
+        if constexpr (sizeof(T) == 4) {
+            const int i = lane % 16, g = lane / 16;
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = *(const float*)(m + tb(b, t) * 1024 + slot(i / 4, 4 * g + e) * 16 + 4 * (i % 4));
+            return v;
+        } else {
+            typedef short s4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s4 lds_s4;
+            const char* a = m + part * 1024 + slot(lane % 4, 4 * (lane / 16) + lane % 16 / 4) * 16 + 8 * (t % 2);
+            const bf16x4 lo = __builtin_bit_cast(
+                bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(a + tb(2 * b, t / 2) * (PARTS * 1024))));
+            const bf16x4 hi = __builtin_bit_cast(
+                bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(a + tb(2 * b + 1, t / 2) * (PARTS * 1024))));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    }
+};
+
+// A matrix of a chunk by rows in LDS: for each part 64 columns, in the order of an operand's k slots: column 32 b + 16 e
+// + 4 g + r stands at 32 b + 8 g + 4 e + r (float32: as it is).
+template <typename T, int PARTS>
+struct GdRowsMat {
     static constexpr int D = GD_Q * PARTS, PITCH = GdRows<T, D>::PITCH;
     // row operand of tile t, columns of k block b
     __device__ static __forceinline__ typename Mma<T>::Frag row(const T* m, int t, int b, int part, int lane) {
@@ -162,17 +311,15 @@ inline LaPlan gd_plan(const GdArgs& a) {
     return p;
 }
 
-// Per-token factors of a chunk in LDS.
+// Per-token factors of a chunk in LDS: e^c, e^(C - c) (-1 behind a value that is not finite), beta; zeros
+// where there is no token.
 struct GdScalars {
-    float in[GD_Q], out[GD_Q], beta[GD_Q];  // e^c, e^(C - c), beta
-    int bad;                                // first row with a value that is not finite, or GD_Q
+    float in[GD_Q], out[GD_Q], beta[GD_Q];
 };
-__device__ __forceinline__ void gd_scalars_store(GdScalars* s, f32x4 v) {  // by the first wave
-    s->in[threadIdx.x] = v[0];
-    s->out[threadIdx.x] = v[1];
-    s->beta[threadIdx.x] = v[2];
-    const unsigned long long bad = __ballot(v[3] != 0.f);
-    if (threadIdx.x == 0) s->bad = bad ? __ffsll(bad) - 1 : GD_Q;
+__device__ __forceinline__ void gd_scalars_fetch(const GdArgs& a, int64_t row0, int n, unsigned lds, int wave, int lane) {
+    const int i = wave < 2 ? wave : 2;  // the last two waves bring the same
+    const float* p = i == 0 ? a.in : (i == 1 ? a.out : a.beta_of);
+    gd_dma4(gd_rsrc(p + row0, n * 4), lds + i * GD_Q * 4, lane * 4);
 }
 
 }  // namespace ssd

@@ -7,28 +7,25 @@
 namespace ssd {
 
 template <typename T, int BD, int CT, int PT>
-constexpr int gd_back_lds() {
-    constexpr int e = sizeof(T);
-    return GD_Q * (GdRows<T, BD>::PITCH * 2 + GdRows<T, 64 * CT>::PITCH + GdMat<T, PT>::PITCH * 2) * e +
-           (int)sizeof(GdScalars) + 16;
-}
+struct GdBackLds {
+    static constexpr int k = 0, q = k + GdTile<T, BD>::BYTES, d = q + GdTile<T, BD>::BYTES,
+                         t = d + GdTile<T, 64 * CT>::BYTES, p = t + GdMat<T, PT>::BYTES,
+                         sc = p + GdMat<T, PT>::BYTES, bytes = (sc + (int)sizeof(GdScalars) + 1023) / 1024 * 1024;
+    static constexpr int buffers = 2 * bytes <= 160 * 1024 ? 2 : 1;
+};
 
 // The gradient G of the state, as the forward walk keeps S: a wave owns columns of G^T.
 template <typename T, int BD, int CT, int PT>
 __global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
     typedef Mma<T> M;
     typedef typename M::Frag Frag;
-    constexpr int SL = M::SL, KS = M::KS, KB = BD / KS, TPK = LaCfg<T>::TPK, NK = GD_Q / KS;
-    constexpr int BT = BD / 16, CDW = 64 * CT;
+    typedef GdBackLds<T, BD, CT, PT> L;
+    typedef GdTile<T, BD> Tile;
+    typedef GdTile<T, 64 * CT> TileV;
     typedef GdMat<T, PT> Mat;
-    constexpr int AP = GdRows<T, BD>::PITCH, CP = GdRows<T, CDW>::PITCH;
-    __shared__ __align__(16) unsigned char lds[gd_back_lds<T, BD, CT, PT>()];
-    T* sk = (T*)lds;
-    T* sq = sk + GD_Q * AP;
-    T* sd = sq + GD_Q * AP;
-    T* st = sd + GD_Q * CP;
-    T* sp = st + GD_Q * Mat::PITCH;
-    GdScalars* sc = (GdScalars*)(sp + GD_Q * Mat::PITCH);
+    constexpr int KS = M::KS, KB = BD / KS, TPK = LaCfg<T>::TPK, NK = GD_Q / KS;
+    constexpr int BT = BD / 16, CDW = 64 * CT;
+    __shared__ __align__(1024) char lds[L::buffers * L::bytes];
 
     const int nblk = a.valdim / CDW;
     const GdItem it = gd_item(a, nblk);
@@ -43,23 +40,44 @@ __global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
     const T* pd = (const T*)a.dout + (int64_t)h * DV + c0;
     const int64_t hrow = (int64_t)h * a.tokens;
 
-    GdRows<T, BD> rk, rq;
-    GdRows<T, CDW> rd;
-    GdRows<T, Mat::D> rt, rp;
-    f32x4 rs;
     auto tokens_of = [&](int k) { return len - k * GD_Q < GD_Q ? len - k * GD_Q : GD_Q; };
-    auto load = [&](int k) {
-        const int n = tokens_of(k);
-        const int64_t t0 = lo + (int64_t)k * GD_Q;
-        rk.load(pk, a.k_ts, t0, n);
-        rq.load(pq, a.q_ts, t0, n);
-        rd.load(pd, a.o_ts, t0, n);
-        rt.load((const T*)a.T, Mat::D, hrow + t0, n);
-        rp.load((const T*)a.P, Mat::D, hrow + t0, n);
-        rs = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (threadIdx.x < n) rs = a.sc[hrow + t0 + threadIdx.x];
+    // as in the forward walk
+    struct Next {
+        gd_i4 k, d, t, q, p;
+        int64_t row;
+        int n;
+        unsigned to;
     };
-    if (nch > 0) load(nch - 1);
+    auto next_of = [&](int k, int buffer) {
+        Next x;
+        const int64_t t0 = lo + (int64_t)k * GD_Q;
+        x.n = tokens_of(k);
+        x.row = hrow + t0;
+        x.to = gd_lds(lds + (L::buffers == 2 && buffer % 2 ? L::bytes : 0));
+        auto rows = [&](const T* base, int64_t ts) { return gd_rsrc(base + t0 * ts, x.n * (int)ts * (int)sizeof(T)); };
+        x.k = rows(pk, a.k_ts);
+        x.q = rows(pq, a.q_ts);
+        x.d = rows(pd, a.o_ts);
+        x.t = gd_rsrc((const T*)a.T + x.row * Mat::D, x.n * Mat::ROW);
+        x.p = gd_rsrc((const T*)a.P + x.row * Mat::D, x.n * Mat::ROW);
+        return x;
+    };
+    constexpr int NR = Tile::FETCHES, NM = Mat::FETCHES, NV = TileV::FETCHES, NF = 2 * NR + 2 * NM + NV + 1;
+    auto fetch = [&](const Next& x, auto I) {
+        constexpr int i = decltype(I)::value, at_d = NR, at_p = at_d + NV, at_t = at_p + NM, at_q = at_t + NM;
+        const int es = (int)sizeof(T);
+        if constexpr (i < at_d) Tile::fetch(x.k, (int)a.k_ts * es, x.to + L::k, i, wave, lane);
+        else if constexpr (i < at_p) TileV::fetch(x.d, (int)a.o_ts * es, x.to + L::d, i - at_d, wave, lane);
+        else if constexpr (i < at_t) Mat::fetch(x.p, x.to + L::p, i - at_p, wave, lane);
+        else if constexpr (i < at_q) Mat::fetch(x.t, x.to + L::t, i - at_t, wave, lane);
+        else if constexpr (i < at_q + NR) Tile::fetch(x.q, (int)a.q_ts * es, x.to + L::q, i - at_q, wave, lane);
+        else gd_scalars_fetch(a, x.row, x.n, x.to + L::sc, wave, lane);
+    };
+    auto stage_all = [&](int k) {
+        const Next x = next_of(k, k);
+        gd_for<NF>([&](auto I) { fetch(x, I); });
+    };
+    if (L::buffers == 2 && nch > 0) stage_all(nch - 1);
 
     f32x4 G[BT][CT];
     const int cw = wave * 16 * CT, col = c0 + cw + lr;
@@ -74,15 +92,14 @@ __global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
     for (int k = nch - 1; k >= 0; --k) {
         const int n = tokens_of(k);
         const int64_t t0 = lo + (int64_t)k * GD_Q;
-        __syncthreads();  // the last chunk's reads are done
-        rk.store(sk);
-        rq.store(sq);
-        rd.store(sd);
-        rt.store(st);
-        rp.store(sp);
-        if (wave == 0) gd_scalars_store(sc, rs);
+        if constexpr (L::buffers == 1) {
+            __syncthreads();  // the last chunk's reads are done
+            stage_all(k);
+        }
+        // behind this chunk's fetches stand only the last chunk's stores of Z
+        if (L::buffers == 2 && k + 1 < nch) gd_wait<16 * CT>();
+        else gd_wait<0>();
         __syncthreads();
-        load(k > 0 ? k - 1 : 0);
         if (k + 1 < nch) {  // the gradient behind chunk k is kept where the state that enters k + 1 is
             float* g = a.G + (la_place(a, plan, it.s, lo, k + 1) * a.H + h) * ((int64_t)BD * DV);
 #pragma unroll
@@ -92,15 +109,35 @@ __global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) g[(la_channel<T>(t, lg) + r) * DV + col + 16 * u] = G[t][u][r];
         }
+        const Next nx = next_of(k > 0 ? k - 1 : 0, k + 1);
+        constexpr int PLACES = KB + 2 * NK;
+        auto ahead = [&](auto I) {
+            constexpr int i = decltype(I)::value, from = i * NF / PLACES, to = (i + 1) * NF / PLACES;
+            if constexpr (L::buffers == 2) gd_for<to - from>([&](auto J) { fetch(nx, std::integral_constant<int, from + decltype(J)::value>{}); });
+        };
+        const char* buf = lds + (L::buffers == 2 && k % 2 ? L::bytes : 0);
+        const char *sk = buf + L::k, *sq = buf + L::q, *sd = buf + L::d, *st = buf + L::t, *sp = buf + L::p;
+        const GdScalars* sc = (const GdScalars*)(buf + L::sc);
 
-        // e^(C - c) K G^T + P^T do
-        f32x4 x[GD_NT][CT];
+        // P^T do + e^(C - c) K G^T
+        f32x4 x[GD_NT][CT], y[GD_NT][CT];
 #pragma unroll
         for (int t = 0; t < GD_NT; ++t)
 #pragma unroll
-            for (int u = 0; u < CT; ++u) x[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int u = 0; u < CT; ++u) x[t][u] = y[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        Frag df[NK][CT];
 #pragma unroll
-        for (int q = 0; q < KB; ++q) {
+        for (int b = 0; b < NK; ++b)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) df[b][u] = TileV::xt(sd, KS * b, cw + 16 * u, lane);
+        Frag f[KB][GD_NT];
+#pragma unroll
+        for (int q = 0; q < KB; ++q)
+#pragma unroll
+            for (int t = 0; t < GD_NT; ++t) f[q][t] = Tile::row(sk, t, q, lane);
+        if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+        gd_for<KB>([&](auto Q) {
+            constexpr int q = decltype(Q)::value;
             Frag gf[CT][PT];
 #pragma unroll
             for (int u = 0; u < CT; ++u) {
@@ -110,33 +147,34 @@ __global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
                 gd_split<T, PT>(tl, gf[u]);
             }
 #pragma unroll
-            for (int t = 0; t < GD_NT; ++t) {
-                const Frag f = M::load(sk + (16 * t + lr) * AP + KS * q + SL * lg);
+            for (int p = PT - 1; p >= 0; --p)
 #pragma unroll
-                for (int u = 0; u < CT; ++u) x[t][u] = gd_mma<T, 1, PT>(&f, gf[u], x[t][u]);
-            }
-        }
+                for (int t = 0; t < GD_NT; ++t)
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) y[t][u] = M::mma(f[q][t], gf[u][p], y[t][u]);
+            ahead(Q);
+        });
+        gd_for<NK>([&](auto B) {
+            constexpr int b = decltype(B)::value;
+            Frag pf[GD_NT][PT];
+#pragma unroll
+            for (int t = 0; t < (b + 1) * TPK; ++t)
+#pragma unroll
+                for (int p = 0; p < PT; ++p) pf[t][p] = Mat::col(sp, t, b, p, lane);
+            ahead(std::integral_constant<int, KB + b>{});
+#pragma unroll
+            for (int p = PT - 1; p >= 0; --p)
+#pragma unroll
+                for (int t = 0; t < (b + 1) * TPK; ++t)
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) x[t][u] = M::mma(pf[t][p], df[b][u], x[t][u]);
+        });
 #pragma unroll
         for (int t = 0; t < GD_NT; ++t) {
             const f32x4 w = *(const f32x4*)(sc->out + 16 * t + 4 * lg);
 #pragma unroll
-            for (int u = 0; u < CT; ++u) x[t][u] *= w;
+            for (int u = 0; u < CT; ++u) x[t][u] += w * y[t][u];
         }
-        Frag df[NK][CT];
-#pragma unroll
-        for (int b = 0; b < NK; ++b)
-#pragma unroll
-            for (int u = 0; u < CT; ++u) df[b][u] = XT<T>::load(sd, CP, KS * b, cw + 16 * u, lane);
-#pragma unroll
-        for (int b = 0; b < NK; ++b)
-#pragma unroll
-            for (int t = 0; t < (b + 1) * TPK; ++t) {
-                Frag pf[PT];
-#pragma unroll
-                for (int p = 0; p < PT; ++p) pf[p] = Mat::col(sp, t, b, p, lane);
-#pragma unroll
-                for (int u = 0; u < CT; ++u) x[t][u] = gd_mma<T, PT, 1>(pf, &df[b][u], x[t][u]);
-            }
 
         // Z = T^T of that
         f32x4 z[GD_NT][CT];
@@ -144,8 +182,8 @@ __global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
         for (int t = 0; t < GD_NT; ++t)
 #pragma unroll
             for (int u = 0; u < CT; ++u) z[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int b = 0; b < NK; ++b) {
+        gd_for<NK>([&](auto B) {
+            constexpr int b = NK - 1 - decltype(B)::value;
             Frag xf[CT][PT];
 #pragma unroll
             for (int u = 0; u < CT; ++u) {
@@ -154,15 +192,21 @@ __global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
                 for (int e = 0; e < TPK; ++e) tl[e] = x[b * TPK + e][u];
                 gd_split<T, PT>(tl, xf[u]);
             }
+            Frag tf[GD_NT][PT];
 #pragma unroll
-            for (int t = 0; t < (b + 1) * TPK; ++t) {
-                Frag tf[PT];
+            for (int t = 0; t < (b + 1) * TPK; ++t)
 #pragma unroll
-                for (int p = 0; p < PT; ++p) tf[p] = Mat::col(st, t, b, p, lane);
+                for (int p = 0; p < PT; ++p) tf[t][p] = Mat::col(st, t, b, p, lane);
+            ahead(std::integral_constant<int, KB + NK + decltype(B)::value>{});
 #pragma unroll
-                for (int u = 0; u < CT; ++u) z[t][u] = gd_mma<T, PT, PT>(tf, xf[u], z[t][u]);
-            }
-        }
+            for (int s = PT - 1; s >= 0; --s)
+#pragma unroll
+                for (int p = 0; p <= s; ++p)
+#pragma unroll
+                    for (int t = 0; t < (b + 1) * TPK; ++t)
+#pragma unroll
+                        for (int u = 0; u < CT; ++u) z[t][u] = M::mma(tf[t][p], xf[u][s - p], z[t][u]);
+        });
         const __amdgpu_buffer_rsrc_t r = buf_rsrc(a.Z + (hrow + t0) * DV, n * DV * 4);
 #pragma unroll
         for (int t = 0; t < GD_NT; ++t)
@@ -179,8 +223,8 @@ __global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
         for (int t = 0; t < BT; ++t)
 #pragma unroll
             for (int u = 0; u < CT; ++u) G[t][u] *= keep;
-#pragma unroll
-        for (int b = 0; b < NK; ++b) {
+        gd_for<NK>([&](auto B) {
+            constexpr int b = decltype(B)::value;
             Frag wf[CT][PT], zf[CT][PT];
 #pragma unroll
             for (int u = 0; u < CT; ++u) {
@@ -199,18 +243,26 @@ __global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
                 gd_split<T, PT>(tl, wf[u]);
                 gd_split<T, PT>(tz, zf[u]);
             }
+            Frag fb[BT];
 #pragma unroll
-            for (int t = 0; t < BT; ++t) {
-                const Frag f = la_bt<T>(sq, AP, KS * b, t, lane);
-                const Frag e = la_bt<T>(sk, AP, KS * b, t, lane);
+            for (int t = 0; t < BT; ++t) fb[t] = Tile::bt(sq, KS * b, t, lane);
 #pragma unroll
-                for (int u = 0; u < CT; ++u) {
-                    G[t][u] = gd_mma<T, 1, PT>(&f, wf[u], G[t][u]);
-                    G[t][u] = gd_mma<T, 1, PT>(&e, zf[u], G[t][u]);
-                }
-            }
-        }
+            for (int p = PT - 1; p >= 0; --p)
+#pragma unroll
+                for (int t = 0; t < BT; ++t)
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) G[t][u] = M::mma(fb[t], wf[u][p], G[t][u]);
+#pragma unroll
+            for (int t = 0; t < BT; ++t) fb[t] = Tile::bt(sk, KS * b, t, lane);
+#pragma unroll
+            for (int p = PT - 1; p >= 0; --p)
+#pragma unroll
+                for (int t = 0; t < BT; ++t)
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) G[t][u] = M::mma(fb[t], zf[u][p], G[t][u]);
+        });
     }
+    gd_wait<0>();  // a workgroup's LDS is another's once its waves have ended
     if (a.dinit) {
 #pragma unroll
         for (int t = 0; t < BT; ++t)
@@ -227,7 +279,7 @@ template <typename T, int DK, int DV>
 struct GdChunkLds {
     typedef GdParts<T> P;
     static constexpr int AP = GdRows<T, DK, DK * 4>::PITCH, VP = DV + 16 / (int)sizeof(T);
-    static constexpr int EP = GdMat<T, P::E>::PITCH, NP = GdMat<T, P::N>::PITCH;
+    static constexpr int EP = GdRowsMat<T, P::E>::PITCH, NP = GdRowsMat<T, P::N>::PITCH;
     static constexpr bool DO = sizeof(T) == 2;  // rows of do are staged too
     // E and N take the place of U and Z
     static constexpr int uz = GD_Q * VP * (P::U + P::Z), en = GD_Q * (EP + NP);
@@ -259,8 +311,8 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
     typedef typename M::Frag Frag;
     typedef GdParts<T> P;
     typedef GdChunkLds<T, DK, DV> L;
-    typedef GdMat<T, P::E> MatE;
-    typedef GdMat<T, P::N> MatN;
+    typedef GdRowsMat<T, P::E> MatE;
+    typedef GdRowsMat<T, P::N> MatN;
     constexpr int SL = M::SL, KS = M::KS, TPK = LaCfg<T>::TPK, NK = GD_Q / KS, KV = DV / KS;
     constexpr int NW = L::NW, NTHR = DK * 4, AP = L::AP, VP = L::VP;
     constexpr int TILES = NK * (NK + 1) / 2 * TPK * TPK;  // of E: whole k blocks on and below the diagonal
@@ -299,10 +351,9 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
         if (m > 0) __syncthreads();  // the last head's reads are done
         if (threadIdx.x < GD_Q) {
             const bool live = threadIdx.x < n;
-            const f32x4 s = live ? a.sc[row0 + threadIdx.x] : f32x4{0.f, 0.f, 1.f, 0.f};
-            s_in[threadIdx.x] = s[0];
-            s_out[threadIdx.x] = s[1];
-            s_beta[threadIdx.x] = s[2];
+            s_in[threadIdx.x] = live ? a.in[row0 + threadIdx.x] : 0.f;
+            s_out[threadIdx.x] = live ? a.out[row0 + threadIdx.x] : 0.f;
+            s_beta[threadIdx.x] = live ? a.beta_of[row0 + threadIdx.x] : 1.f;
             c2[threadIdx.x] = live ? a.c2[row0 + threadIdx.x] : -1e30;  // no factor of a row without a token
         }
         const T* pd = (const T*)a.dout + t0 * a.o_ts + (int64_t)h * DV;
@@ -324,7 +375,7 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
                 z[e] = buf_load<f32x4>(rz, (row * DV + c + 4 * e) * 4);
             }
             const int live = row < n;
-            const float be = live ? a.sc[row0 + row][2] : 1.f;
+            const float be = live ? a.beta_of[row0 + row] : 1.f;
             float v[8], dv[8], zu = 0.f, vz = 0.f;
             gd_eight((const T*)a.v + (t0 + (live ? row : 0)) * a.v_ts + (int64_t)h * DV + c, v);
 #pragma unroll

@@ -17,7 +17,7 @@ static GdBwdWs bwd_layout(const GdArgs& a, int act) {
     w.T = 0;
     w.P = align256(w.T + mat);
     w.sc = align256(w.P + mat);
-    w.c2 = align256(w.sc + rows * sizeof(f32x4));
+    w.c2 = align256(w.sc + rows * 3 * sizeof(float));
     w.U = align256(w.c2 + rows * sizeof(double));
     w.Z = align256(w.U + rows * a.valdim * 4);
     w.S = align256(w.Z + rows * a.valdim * 4);
@@ -48,7 +48,9 @@ hipError_t launch_gd_bwd(GdArgs a, int act, void* ws, hipStream_t s) {
     const GdBwdWs w = bwd_layout(a, act);
     char* p = (char*)ws;
     a.T = p + w.T, a.P = p + w.P;
-    a.sc = (f32x4*)(p + w.sc), a.c2 = (double*)(p + w.c2);
+    a.in = (float*)(p + w.sc), a.c2 = (double*)(p + w.c2);
+    a.out = a.in + (size_t)a.H * a.tokens;
+    a.beta_of = a.out + (size_t)a.H * a.tokens;
     a.U = (float*)(p + w.U), a.Z = (float*)(p + w.Z);
     a.S = (float*)(p + w.S), a.G = (float*)(p + w.G);
     return act == SSD_BF16 ? bwd_t<bf16>(a, s) : bwd_t<float>(a, s);

@@ -14,7 +14,7 @@ static GdFwdWs fwd_layout(const GdArgs& a, int act) {
     w.T = 0;
     w.P = align256(w.T + rows * GD_Q * (act == SSD_BF16 ? 3 : 1) * e);
     w.sc = align256(w.P + rows * GD_Q * (act == SSD_BF16 ? 2 : 1) * e);
-    w.total = align256(w.sc + rows * sizeof(f32x4));
+    w.total = align256(w.sc + rows * 3 * sizeof(float));
     return w;
 }
 size_t gd_fwd_ws(const GdArgs& a, int act) { return fwd_layout(a, act).total; }
@@ -42,7 +42,9 @@ hipError_t launch_gd_fwd(GdArgs a, int act, void* ws, hipStream_t s) {
     const GdFwdWs w = fwd_layout(a, act);
     a.T = (char*)ws + w.T;
     a.P = (char*)ws + w.P;
-    a.sc = (f32x4*)((char*)ws + w.sc);
+    a.in = (float*)((char*)ws + w.sc);
+    a.out = a.in + (size_t)a.H * a.tokens;
+    a.beta_of = a.out + (size_t)a.H * a.tokens;
     return act == SSD_BF16 ? fwd_t<bf16>(a, s) : fwd_t<float>(a, s);
 }
 

@@ -16,7 +16,7 @@ namespace ssd {
 constexpr float GD_BETA_MIN = 9.094947017729282e-13f;  // 2^-40
 
 // PT, PP: parts of T and P.  TAME: a key, g or beta that is not finite ends the chunk at its row (k and
-// beta count as zero from there on, and the row is told by sc); else it spreads over the chunk.
+// beta count as zero from there on, and `out` tells the rows); else it spreads over the chunk.
 template <typename T, int DK, int PT, int PP, bool TAME>
 __global__ void __launch_bounds__(256) k_gd_prep(GdArgs a, LaPlan plan) {
     typedef Mma<T> M;
@@ -72,8 +72,9 @@ __global__ void __launch_bounds__(256) k_gd_prep(GdArgs a, LaPlan plan) {
         const double last = __shfl(c, 63, 64);
         if (lane < n) {
             const bool bad = TAME && lane >= sbad;
-            a.sc[row0 + lane] = f32x4{__builtin_amdgcn_exp2f((float)c), __builtin_amdgcn_exp2f((float)(last - c)),
-                                      b, bad ? 1.f : 0.f};
+            a.in[row0 + lane] = __builtin_amdgcn_exp2f((float)c);
+            a.out[row0 + lane] = bad ? -1.f : __builtin_amdgcn_exp2f((float)(last - c));
+            a.beta_of[row0 + lane] = b;
             if constexpr (!TAME) a.c2[row0 + lane] = c;
         }
     }

@@ -1,8 +1,11 @@
 // The walk of the gated delta rule from chunk to chunk (see gdelta.h): forward, and the same walk as
 // the backward's recomputation (KEEP), which keeps entering states and u instead of outputs.
 //
-// A workgroup of four waves walks 64 CT value channels of a head over its sequence.  The rows of
-// the next chunk are on their way into registers while a chunk is computed.
+// A workgroup of four waves walks 64 CT value channels of a head over its sequence.  The waves meet once
+// per chunk, where the next chunk's operands have arrived; between, each goes its own way.  With one
+// wave to a SIMD nothing hides an LDS read but the wave's own work: the operands of a product are read
+// while the one before it runs, and the splitting of a result into parts is dealt out between the
+// matrix instructions of the next product (the scheduling groups).
 #pragma once
 
 #include "gdelta.h"
@@ -10,31 +13,28 @@
 namespace ssd {
 
 template <typename T, int BD, int CT, int PT, bool KEEP>
-constexpr int gd_walk_lds() {
-    constexpr int e = sizeof(T);
-    return GD_Q * (GdRows<T, BD>::PITCH * (KEEP ? 1 : 2) + GdRows<T, 64 * CT>::PITCH + GdMat<T, PT>::PITCH +
-                   (KEEP ? 0 : GdMat<T, sizeof(T) == 2 ? 2 : 1>::PITCH)) * e +
-           (int)sizeof(GdScalars) + 16;
-}
+struct GdWalkLds {
+    static constexpr int PO = sizeof(T) == 2 ? 2 : 1;  // parts of P and of what else only meets outputs
+    static constexpr int k = 0, v = k + GdTile<T, BD>::BYTES, t = v + GdTile<T, 64 * CT>::BYTES,
+                         sc = t + GdMat<T, PT>::BYTES, q = sc + (int)sizeof(GdScalars),
+                         p = q + (KEEP ? 0 : GdTile<T, BD>::BYTES),
+                         bytes = (p + (KEEP ? 0 : GdMat<T, PO>::BYTES) + 1023) / 1024 * 1024;
+    static constexpr int buffers = 2 * bytes <= 160 * 1024 ? 2 : 1;
+};
 
 // PT: parts of T, R, states and u on their way into states (2, or 3 where a state is asked for).
 template <typename T, int BD, int CT, int PT, bool KEEP>
 __global__ void __launch_bounds__(256) k_gd_walk(GdArgs a, LaPlan plan) {
     typedef Mma<T> M;
     typedef typename M::Frag Frag;
+    typedef GdWalkLds<T, BD, CT, PT, KEEP> L;
+    typedef GdTile<T, BD> Tile;
+    typedef GdTile<T, 64 * CT> TileV;
     constexpr int SL = M::SL, KS = M::KS, KB = BD / KS, TPK = LaCfg<T>::TPK, NK = GD_Q / KS;
-    constexpr int BT = BD / 16, CDW = 64 * CT, PO = sizeof(T) == 2 ? 2 : 1;  // parts in outputs
-    constexpr int PE = 1;  // q, k and v are exact
+    constexpr int BT = BD / 16, CDW = 64 * CT, PO = L::PO, PE = 1;  // q, k and v are exact
     typedef GdMat<T, PT> MatT;
     typedef GdMat<T, PO> MatP;
-    constexpr int AP = GdRows<T, BD>::PITCH, CP = GdRows<T, CDW>::PITCH;
-    __shared__ __align__(16) unsigned char lds[gd_walk_lds<T, BD, CT, PT, KEEP>()];
-    T* sk = (T*)lds;
-    T* sv = sk + GD_Q * AP;
-    T* st = sv + GD_Q * CP;
-    T* sq = st + GD_Q * MatT::PITCH;
-    T* sp = sq + (KEEP ? 0 : GD_Q * AP);
-    GdScalars* sc = (GdScalars*)(sp + (KEEP ? 0 : GD_Q * MatP::PITCH));
+    __shared__ __align__(1024) char lds[L::buffers * L::bytes];
 
     const int nblk = a.valdim / CDW;
     const GdItem it = gd_item(a, nblk);
@@ -49,26 +49,48 @@ __global__ void __launch_bounds__(256) k_gd_walk(GdArgs a, LaPlan plan) {
     const T* pv = (const T*)a.v + (int64_t)h * DV + c0;
     const int64_t hrow = (int64_t)h * a.tokens;
 
-    GdRows<T, BD> rk, rq;
-    GdRows<T, CDW> rv;
-    GdRows<T, MatT::D> rt;
-    GdRows<T, MatP::D> rp;
-    f32x4 rs;
     auto tokens_of = [&](int k) { return len - k * GD_Q < GD_Q ? len - k * GD_Q : GD_Q; };
-    auto load = [&](int k) {
-        const int n = tokens_of(k);
-        const int64_t t0 = lo + (int64_t)k * GD_Q;
-        rk.load(pk, a.k_ts, t0, n);
-        rv.load(pv, a.v_ts, t0, n);
-        rt.load((const T*)a.T, MatT::D, hrow + t0, n);
-        if constexpr (!KEEP) {
-            rq.load(pq, a.q_ts, t0, n);
-            rp.load((const T*)a.P, MatP::D, hrow + t0, n);
-        }
-        rs = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (threadIdx.x < n) rs = a.sc[hrow + t0 + threadIdx.x];
+    // The operands of chunk k, a fetch of each wave at a time: all at once they would hold up the waves
+    // until the CU has accepted them.  The last chunk fetches itself again, so that no branch parts the code.
+    struct Next {
+        gd_i4 k, v, t, q, p;
+        int64_t row;
+        int n;
+        unsigned to;
     };
-    if (nch > 0) load(0);
+    auto next_of = [&](int k, int buffer) {
+        Next x;
+        const int64_t t0 = lo + (int64_t)k * GD_Q;
+        x.n = tokens_of(k);
+        x.row = hrow + t0;
+        x.to = gd_lds(lds + (L::buffers == 2 && buffer % 2 ? L::bytes : 0));
+        auto rows = [&](const T* base, int64_t ts) { return gd_rsrc(base + t0 * ts, x.n * (int)ts * (int)sizeof(T)); };
+        x.k = rows(pk, a.k_ts);
+        x.v = rows(pv, a.v_ts);
+        x.t = gd_rsrc((const T*)a.T + x.row * MatT::D, x.n * MatT::ROW);
+        if constexpr (!KEEP) {
+            x.q = rows(pq, a.q_ts);
+            x.p = gd_rsrc((const T*)a.P + x.row * MatP::D, x.n * MatP::ROW);
+        }
+        return x;
+    };
+    constexpr int NK_ = Tile::FETCHES, NV = TileV::FETCHES, NQ = KEEP ? 0 : NK_, NP = KEEP ? 0 : MatP::FETCHES;
+    constexpr int NF = NK_ + MatT::FETCHES + NV + NP + NQ + 1;
+    auto fetch = [&](const Next& x, auto I) {
+        constexpr int i = decltype(I)::value, at_t = NK_, at_v = at_t + MatT::FETCHES, at_p = at_v + NV, at_q = at_p + NP;
+        const int es = (int)sizeof(T);
+        if constexpr (i < at_t) Tile::fetch(x.k, (int)a.k_ts * es, x.to + L::k, i, wave, lane);
+        else if constexpr (i < at_v) MatT::fetch(x.t, x.to + L::t, i - at_t, wave, lane);
+        else if constexpr (i < at_p) TileV::fetch(x.v, (int)a.v_ts * es, x.to + L::v, i - at_v, wave, lane);
+        else if constexpr (i < at_q) MatP::fetch(x.p, x.to + L::p, i - at_p, wave, lane);
+        else if constexpr (i < at_q + NQ) Tile::fetch(x.q, (int)a.q_ts * es, x.to + L::q, i - at_q, wave, lane);
+        else gd_scalars_fetch(a, x.row, x.n, x.to + L::sc, wave, lane);
+    };
+    auto stage_all = [&](int k) {
+        const Next x = next_of(k, k);
+        gd_for<NF>([&](auto I) { fetch(x, I); });
+    };
+    if (L::buffers == 2 && nch > 0) stage_all(0);
 
     // this lane's elements of tile (t, u): channels of k from la_channel, channel `col` + 16 u of v
     f32x4 St[BT][CT];
@@ -84,33 +106,84 @@ __global__ void __launch_bounds__(256) k_gd_walk(GdArgs a, LaPlan plan) {
     for (int k = 0; k < nch; ++k) {
         const int n = tokens_of(k);
         const int64_t t0 = lo + (int64_t)k * GD_Q;
-        __syncthreads();  // the last chunk's reads are done
-        rk.store(sk);
-        rv.store(sv);
-        rt.store(st);
-        if constexpr (!KEEP) {
-            rq.store(sq);
-            rp.store(sp);
+        if constexpr (L::buffers == 1) {
+            __syncthreads();  // the last chunk's reads are done
+            stage_all(k);
         }
-        if (wave == 0) gd_scalars_store(sc, rs);
+        // behind this chunk's fetches stand only the last chunk's stores of u or of outputs
+        constexpr int STORES = (KEEP ? 16 : (sizeof(T) == 2 ? 2 : 4)) * CT;
+        if (L::buffers == 2 && k > 0) gd_wait<STORES>();
+        else gd_wait<0>();
         __syncthreads();
-        load(k + 1 < nch ? k + 1 : k);
-        const int bad = sc->bad;
-        if (!KEEP && bad < GD_Q) {  // for the whole workgroup
-            for (int x = threadIdx.x; x < (GD_Q - bad) * AP; x += 256) sk[bad * AP + x] = (T)0.f;
-            __syncthreads();
+        if (KEEP && k > 0) {
+            float* S = a.S + (la_place(a, plan, it.s, lo, k) * a.H + h) * ((int64_t)BD * DV);
+#pragma unroll
+            for (int t = 0; t < BT; ++t)
+#pragma unroll
+                for (int u = 0; u < CT; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[(la_channel<T>(t, lg) + r) * DV + col + 16 * u] = St[t][u][r];
         }
-        if constexpr (KEEP)
-            if (k > 0) {
-                float* S = a.S + (la_place(a, plan, it.s, lo, k) * a.H + h) * ((int64_t)BD * DV);
+        const Next nx = next_of(k + 1 < nch ? k + 1 : k, k + 1);
+        // the fetches of the I-th of N places in what follows
+        constexpr int PLACES = KEEP ? KB + 3 : 2 * KB + 3 + 2 * NK;
+        auto ahead = [&](auto I) {
+            constexpr int i = decltype(I)::value, from = i * NF / PLACES, to = (i + 1) * NF / PLACES;
+            if constexpr (L::buffers == 2) gd_for<to - from>([&](auto J) { fetch(nx, std::integral_constant<int, from + decltype(J)::value>{}); });
+        };
+        char* buf = lds + (L::buffers == 2 && k % 2 ? L::bytes : 0);
+        char* sk = buf + L::k;
+        const char *sv = buf + L::v, *st = buf + L::t, *sq = buf + L::q, *sp = buf + L::p;
+        const GdScalars* sc = (const GdScalars*)(buf + L::sc);
+
+        // A value of v that is not finite would reach the rows before its own: it counts as zero, and its
+        // channel is made NaN from its row on further down; so is every channel from a row that prep
+        // found bad.
+        Frag vf[NK][CT];
+        int first[CT];
+        bool tame = true;
 #pragma unroll
-                for (int t = 0; t < BT; ++t)
+        for (int b = 0; b < NK; ++b)
 #pragma unroll
-                    for (int u = 0; u < CT; ++u)
+            for (int u = 0; u < CT; ++u) vf[b][u] = TileV::xt(sv, KS * b, cw + 16 * u, lane);
+        if constexpr (!KEEP) {
+            const unsigned long long bad = __ballot(sc->out[lane] < 0.f);
+            float seen = 0.f;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            S[(la_channel<T>(t, lg) + r) * DV + col + 16 * u] = St[t][u][r];
+            for (int b = 0; b < NK; ++b)
+#pragma unroll
+                for (int u = 0; u < CT; ++u)
+#pragma unroll
+                    for (int s = 0; s < SL; ++s) seen = __builtin_fmaf((float)vf[b][u][s], 0.f, seen);
+            tame = !bad && __ballot(seen != 0.f) == 0;  // NaN is not equal to zero
+            if (!tame) {
+#pragma unroll
+                for (int u = 0; u < CT; ++u) {
+                    first[u] = bad ? __ffsll(bad) - 1 : GD_Q;
+#pragma unroll
+                    for (int b = NK - 1; b >= 0; --b)
+#pragma unroll
+                        for (int s = SL - 1; s >= 0; --s)
+                            if (!(fabsf((float)vf[b][u][s]) < INFINITY)) {
+                                const int j = KS * b + 16 * (s / 4) + 4 * lg + s % 4;
+                                first[u] = j < first[u] ? j : first[u];
+                                vf[b][u][s] = (T)0.f;
+                            }
+                    // the least of the four lane groups' rows
+#pragma unroll
+                    for (int m = 16; m < 64; m <<= 1) {
+                        const int y = __shfl_xor(first[u], m, 64);
+                        first[u] = y < first[u] ? y : first[u];
+                    }
+                }
             }
+            if (bad) {  // for the whole workgroup
+                const int row = __ffsll(bad) - 1;
+                for (int x = threadIdx.x; x < (GD_Q - row) * Tile::RB / 16; x += 256)
+                    *(f32x4*)(sk + row * Tile::RB + x * 16) = f32x4{0.f, 0.f, 0.f, 0.f};
+                __syncthreads();
+            }
+        }
 
         // X = K S^T and S Q^T
         f32x4 x[GD_NT][CT], o[GD_NT][CT];
@@ -118,65 +191,51 @@ __global__ void __launch_bounds__(256) k_gd_walk(GdArgs a, LaPlan plan) {
         for (int t = 0; t < GD_NT; ++t)
 #pragma unroll
             for (int u = 0; u < CT; ++u) x[t][u] = o[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        Frag sf[KB][CT][PT], f[KB][GD_NT];
 #pragma unroll
-        for (int q = 0; q < KB; ++q) {
-            Frag sf[CT][PT];
+        for (int q = 0; q < KB; ++q)
+#pragma unroll
+            for (int t = 0; t < GD_NT; ++t) f[q][t] = Tile::row(sk, t, q, lane);
+        if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+        gd_for<KB>([&](auto Q) {
+            constexpr int q = decltype(Q)::value;
 #pragma unroll
             for (int u = 0; u < CT; ++u) {
                 f32x4 tl[TPK];
 #pragma unroll
                 for (int e = 0; e < TPK; ++e) tl[e] = St[q * TPK + e][u];
-                gd_split<T, PT>(tl, sf[u]);
+                gd_split<T, PT>(tl, sf[q][u]);
             }
 #pragma unroll
-            for (int t = 0; t < GD_NT; ++t) {
-                const Frag f = M::load(sk + (16 * t + lr) * AP + KS * q + SL * lg);
+            for (int p = PT - 1; p >= 0; --p)
 #pragma unroll
-                for (int u = 0; u < CT; ++u) x[t][u] = gd_mma<T, PE, PT>(&f, sf[u], x[t][u]);
-            }
+                for (int t = 0; t < GD_NT; ++t)
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) x[t][u] = M::mma(f[q][t], sf[q][u][p], x[t][u]);
             if constexpr (!KEEP)
 #pragma unroll
-                for (int t = 0; t < GD_NT; ++t) {
-                    const Frag f = M::load(sq + (16 * t + lr) * AP + KS * q + SL * lg);
+                for (int t = 0; t < GD_NT; ++t) f[q][t] = Tile::row(sq, t, q, lane);
+            ahead(Q);
+        });
+        if constexpr (!KEEP)
+            gd_for<KB>([&](auto Q) {
+                constexpr int q = decltype(Q)::value;
 #pragma unroll
-                    for (int u = 0; u < CT; ++u) o[t][u] = gd_mma<T, PO, PE>(sf[u], &f, o[t][u]);
-                }
-        }
+                for (int p = PO - 1; p >= 0; --p)
+#pragma unroll
+                    for (int t = 0; t < GD_NT; ++t)
+#pragma unroll
+                        for (int u = 0; u < CT; ++u) o[t][u] = M::mma(sf[q][u][p], f[q][t], o[t][u]);
+                ahead(std::integral_constant<int, KB + q>{});
+            });
+        constexpr int AFTER = KEEP ? KB : 2 * KB;
 
-        // R = B (V - e^c X).  A value of v that is not finite would reach the rows before its own: it
-        // counts as zero, and its channel is made NaN from its row on further down.
+        // R = B (V - e^c X), U = T R
         Frag rf[NK][CT][PT];
-        int first[CT];
 #pragma unroll
-        for (int u = 0; u < CT; ++u) {
-            float seen = 0.f;
-            Frag vf[NK];
+        for (int b = 0; b < NK; ++b)
 #pragma unroll
-            for (int b = 0; b < NK; ++b) {
-                vf[b] = XT<T>::load(sv, CP, KS * b, cw + 16 * u, lane);
-#pragma unroll
-                for (int s = 0; s < SL; ++s) seen += (float)vf[b][s] * 0.f;
-            }
-            first[u] = bad;
-            if (!KEEP && __ballot(seen != 0.f)) {  // NaN is not equal to zero
-#pragma unroll
-                for (int b = NK - 1; b >= 0; --b)
-#pragma unroll
-                    for (int s = SL - 1; s >= 0; --s)
-                        if (!(fabsf((float)vf[b][s]) < INFINITY)) {
-                            const int j = KS * b + 16 * (s / 4) + 4 * lg + s % 4;
-                            first[u] = j < first[u] ? j : first[u];
-                            vf[b][s] = (T)0.f;
-                        }
-                // the least of the four lane groups' rows
-#pragma unroll
-                for (int m = 16; m < 64; m <<= 1) {
-                    const int y = __shfl_xor(first[u], m, 64);
-                    first[u] = y < first[u] ? y : first[u];
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < NK; ++b) {
+            for (int u = 0; u < CT; ++u) {
                 f32x4 tl[TPK];
 #pragma unroll
                 for (int e = 0; e < TPK; ++e) {
@@ -184,28 +243,39 @@ __global__ void __launch_bounds__(256) k_gd_walk(GdArgs a, LaPlan plan) {
                     const f32x4 in = *(const f32x4*)(sc->in + 16 * t + 4 * lg);
                     const f32x4 be = *(const f32x4*)(sc->beta + 16 * t + 4 * lg);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) tl[e][r] = be[r] * ((float)vf[b][4 * e + r] - in[r] * x[t][u][r]);
+                    for (int r = 0; r < 4; ++r) tl[e][r] = be[r] * ((float)vf[b][u][4 * e + r] - in[r] * x[t][u][r]);
                 }
                 gd_split<T, PT>(tl, rf[b][u]);
             }
-        }
-
-        // U = T R
 #pragma unroll
         for (int t = 0; t < GD_NT; ++t)
 #pragma unroll
             for (int u = 0; u < CT; ++u) x[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // two row tiles at a time, so that neighbouring instructions do not wait for each other
+        gd_for<2>([&](auto H) {
+            constexpr int h2 = 2 * decltype(H)::value;
 #pragma unroll
-        for (int b = 0; b < NK; ++b)
+            for (int b = 0; b * TPK <= h2 + 1; ++b) {
+                Frag tf[2][PT];
 #pragma unroll
-            for (int t = b * TPK; t < GD_NT; ++t) {
-                Frag tf[PT];
+                for (int e = 0; e < 2; ++e)
+                    if (b * TPK <= h2 + e)
 #pragma unroll
-                for (int p = 0; p < PT; ++p) tf[p] = MatT::row(st, t, b, p, lane);
+                        for (int p = 0; p < PT; ++p) tf[e][p] = MatT::row(st, h2 + e, b, p, lane);
 #pragma unroll
-                for (int u = 0; u < CT; ++u) x[t][u] = gd_mma<T, PT, PT>(tf, rf[b][u], x[t][u]);
+                for (int s = PT - 1; s >= 0; --s)
+#pragma unroll
+                    for (int p = 0; p <= s; ++p)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (b * TPK <= h2 + e)
+#pragma unroll
+                                for (int u = 0; u < CT; ++u)
+                                    x[h2 + e][u] = M::mma(tf[e][p], rf[b][u][s - p], x[h2 + e][u]);
             }
-
+            ahead(std::integral_constant<int, AFTER + decltype(H)::value>{});
+        });
+        ahead(std::integral_constant<int, AFTER + 2>{});
         if constexpr (KEEP) {
             const __amdgpu_buffer_rsrc_t r = buf_rsrc(a.U + (hrow + t0) * DV, n * DV * 4);
 #pragma unroll
@@ -224,8 +294,8 @@ __global__ void __launch_bounds__(256) k_gd_walk(GdArgs a, LaPlan plan) {
 #pragma unroll
                 for (int u = 0; u < CT; ++u) o[t][u] *= f;
             }
-#pragma unroll
-            for (int b = 0; b < NK; ++b) {
+            gd_for<NK>([&](auto B) {
+                constexpr int b = decltype(B)::value;
                 Frag uf[CT][PO];
 #pragma unroll
                 for (int u = 0; u < CT; ++u) {
@@ -234,18 +304,56 @@ __global__ void __launch_bounds__(256) k_gd_walk(GdArgs a, LaPlan plan) {
                     for (int e = 0; e < TPK; ++e) tl[e] = x[b * TPK + e][u];
                     gd_split<T, PO>(tl, uf[u]);
                 }
+                Frag pf[GD_NT][PO];
 #pragma unroll
-                for (int t = b * TPK; t < GD_NT; ++t) {
-                    Frag pf[PO];
+                for (int t = b * TPK; t < GD_NT; ++t)
 #pragma unroll
-                    for (int p = 0; p < PO; ++p) pf[p] = MatP::row(sp, t, b, p, lane);
+                    for (int p = 0; p < PO; ++p) pf[t][p] = MatP::row(sp, t, b, p, lane);
 #pragma unroll
-                    for (int u = 0; u < CT; ++u) o[t][u] = gd_mma<T, PO, PO>(uf[u], pf, o[t][u]);
-                }
+                for (int s = PO - 1; s >= 0; --s)
+#pragma unroll
+                    for (int p = 0; p <= s; ++p)
+#pragma unroll
+                        for (int t = b * TPK; t < GD_NT; ++t)
+#pragma unroll
+                            for (int u = 0; u < CT; ++u) o[t][u] = M::mma(uf[u][p], pf[t][s - p], o[t][u]);
+                ahead(std::integral_constant<int, AFTER + 3 + b>{});
+            });
+        }
+
+        // S <- e^C S + sum_j e^(C - c_j) u_j k_j^T
+        const float keep = sc->in[n - 1];
+#pragma unroll
+        for (int t = 0; t < BT; ++t)
+#pragma unroll
+            for (int u = 0; u < CT; ++u) St[t][u] *= keep;
+        gd_for<NK>([&](auto B) {
+            constexpr int b = decltype(B)::value;
+            Frag uf[CT][PT];
+#pragma unroll
+            for (int u = 0; u < CT; ++u) {
+                f32x4 tl[TPK];
+#pragma unroll
+                for (int e = 0; e < TPK; ++e)
+                    tl[e] = x[b * TPK + e][u] * *(const f32x4*)(sc->out + 16 * (b * TPK + e) + 4 * lg);
+                gd_split<T, PT>(tl, uf[u]);
             }
+            Frag f[BT];
 #pragma unroll
-            for (int u = 0; u < CT; ++u)
-                if (__ballot(first[u] < GD_Q)) {
+            for (int t = 0; t < BT; ++t) f[t] = Tile::bt(sk, KS * b, t, lane);
+            if constexpr (!KEEP) ahead(std::integral_constant<int, AFTER + 3 + NK + b>{});
+#pragma unroll
+            for (int p = PT - 1; p >= 0; --p)
+#pragma unroll
+                for (int t = 0; t < BT; ++t)
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) St[t][u] = M::mma(f[t], uf[u][p], St[t][u]);
+        });
+
+        if constexpr (!KEEP) {
+            if (!tame) {
+#pragma unroll
+                for (int u = 0; u < CT; ++u) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int f = __shfl(first[u], 4 * lg + r, 64);
@@ -253,7 +361,11 @@ __global__ void __launch_bounds__(256) k_gd_walk(GdArgs a, LaPlan plan) {
                         for (int t = 0; t < GD_NT; ++t)
                             if (16 * t + lr >= f) o[t][u][r] = NAN;
                     }
+                    if (first[u] < GD_Q)
+#pragma unroll
+                        for (int t = 0; t < BT; ++t) St[t][u] = f32x4{NAN, NAN, NAN, NAN};
                 }
+            }
             const int out_bytes = (int)a.o_ts * (int)sizeof(T);
             const __amdgpu_buffer_rsrc_t r =
                 buf_rsrc((T*)a.o + t0 * a.o_ts + (int64_t)h * DV + c0, n * out_bytes);
@@ -278,38 +390,8 @@ __global__ void __launch_bounds__(256) k_gd_walk(GdArgs a, LaPlan plan) {
                         buf_store(o[t][u], r, (16 * t + lr) * out_bytes + (cw + 16 * u + 4 * lg) * 4);
             }
         }
-
-        // S <- e^C S + sum_j e^(C - c_j) u_j k_j^T
-        const float keep = sc->in[n - 1];
-#pragma unroll
-        for (int t = 0; t < BT; ++t)
-#pragma unroll
-            for (int u = 0; u < CT; ++u) St[t][u] *= keep;
-#pragma unroll
-        for (int b = 0; b < NK; ++b) {
-            Frag uf[CT][PT];
-#pragma unroll
-            for (int u = 0; u < CT; ++u) {
-                f32x4 tl[TPK];
-#pragma unroll
-                for (int e = 0; e < TPK; ++e)
-                    tl[e] = x[b * TPK + e][u] * *(const f32x4*)(sc->out + 16 * (b * TPK + e) + 4 * lg);
-                gd_split<T, PT>(tl, uf[u]);
-            }
-#pragma unroll
-            for (int t = 0; t < BT; ++t) {
-                const Frag f = la_bt<T>(sk, AP, KS * b, t, lane);
-#pragma unroll
-                for (int u = 0; u < CT; ++u) St[t][u] = gd_mma<T, PE, PT>(&f, uf[u], St[t][u]);
-            }
-        }
-        if (!KEEP)
-#pragma unroll
-            for (int u = 0; u < CT; ++u)
-                if (first[u] < GD_Q)
-#pragma unroll
-                    for (int t = 0; t < BT; ++t) St[t][u] = f32x4{NAN, NAN, NAN, NAN};
     }
+    gd_wait<0>();  // a workgroup's LDS is another's once its waves have ended
     if (!KEEP && a.fin) {
 #pragma unroll
         for (int t = 0; t < BT; ++t)

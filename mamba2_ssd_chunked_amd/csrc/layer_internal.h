@@ -29,7 +29,7 @@ struct GdArgs {
     float scale;
     // workspace
     void *T, *P;                              // [H][tokens][64 columns in parts], see GdMat
-    f32x4* sc;                                // [H][tokens]: e^c, e^(C - c), beta, 1 behind a bad value
+    float *in, *out, *beta_of;                // [H][tokens]: e^c, e^(C - c) (-1: see GdScalars), beta
     double* c2;                               // [H][tokens]: c in units of log 2 (backward)
     float *S, *G;                             // [place][H][DK][DV] states entering, gradients leaving
     float *U, *Z;                             // [H][tokens][DV]
