@@ -80,6 +80,54 @@ __device__ __forceinline__ void gd_for(F&& f) {
     gd_each(std::make_integer_sequence<int, N>{}, f);
 }
 
+// gd_split of eight values in 4 P steps of a few instructions each, to be dealt out between matrix
+// instructions; a pair's next step comes four steps later (a remainder takes a few cycles to arrive).
+template <int P>
+struct GdSplit {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    static constexpr int STEPS = 4 * P;
+    bf16x8 f[P];
+    float x[8];
+    __device__ __forceinline__ void set(f32x4 a, f32x4 b) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = a[e], x[4 + e] = b[e];
+    }
+    template <int I>
+    __device__ __forceinline__ void step(unsigned first, unsigned second) {
+        constexpr int e = I % 4 * 2, p = I / 4;
+        const b2 h = {(bf16)x[e], (bf16)x[e + 1]};
+        f[p][e] = h[0];
+        f[p][e + 1] = h[1];
+        if constexpr (p < P - 1) {
+            x[e] = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(b2, first), x[e], false);
+            x[e + 1] = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(b2, second), x[e + 1], false);
+        }
+    }
+};
+// The combinations of PA and PB parts whose weight counts, small ones first: part I of the list.
+template <int PT>
+struct GdPairs {
+    static constexpr int N = PT * (PT + 1) / 2;
+    static constexpr int sum(int i) { return i < PT ? PT - 1 : (i < 2 * PT - 1 ? PT - 2 : 0); }
+    static constexpr int a(int i) { return i < PT ? i : (i < 2 * PT - 1 ? i - PT : 0); }
+    static constexpr int b(int i) { return sum(i) - a(i); }
+};
+
+// NM matrix instructions m(i) with NW pieces of other work w(i) dealt out evenly behind them, from the
+// LEAD-th on; the compiler keeps the order.  A wave that has its SIMD for itself would else do one after the
+// other.
+template <int NM, int NW, int LEAD, typename FM, typename FW>
+__device__ __forceinline__ void gd_weave(FM&& m, FW&& w) {
+    constexpr int over = NM - LEAD > 0 ? NM - LEAD : 1;
+    gd_for<NM>([&](auto I) {
+        constexpr int i = decltype(I)::value - LEAD;
+        m(I);
+        constexpr int from = i < 0 ? 0 : i * NW / over, to = i < 0 ? 0 : (i + 1) * NW / over;
+        gd_for<to - from>([&](auto J) { w(std::integral_constant<int, from + decltype(J)::value>{}); });
+        __builtin_amdgcn_sched_barrier(0);
+    });
+}
+
 // Rows of D elements of a chunk on their way into LDS, by NTHR threads; rows without a token are
 // zeros (bounded loads).
 template <typename T, int D, int NTHR = 256>
@@ -151,15 +199,16 @@ template <typename T, int D>
 struct GdTile {
     static constexpr int RB = D * (int)sizeof(T), PPR = RB / 16, BYTES = GD_Q * RB;
     __device__ static __forceinline__ int flip(int row) {
-        if constexpr (sizeof(T) == 4) return (4 * ((row >> 2) & 3)) ^ (row & 3);
+        constexpr int m = PPR - 1;
+        if constexpr (sizeof(T) == 4) return ((4 * ((row >> 2) & 3)) ^ (row & 3)) & m;
         else if constexpr (D == 128) return (4 * (row & 3)) ^ (2 * ((row >> 2) & 1));
-        else return (4 * ((row >> 1) & 1)) ^ (2 * ((row >> 2) & 1));
+        else return ((4 * ((row >> 1) & 1)) ^ (2 * ((row >> 2) & 1))) & m;
     }
     __device__ static __forceinline__ int at(int row, int piece) { return row * RB + ((piece ^ flip(row)) << 4); }
-    static constexpr int FETCHES = BYTES / 4096;  // of each of four waves
-    // the j-th fetch of a wave of rows `bytes` apart
-    __device__ static __forceinline__ void fetch(gd_i4 r, int bytes, unsigned lds, int j, int wave, int lane) {
-        const int i = 4 * j + wave, x = i * 64 + lane, row = x / PPR, piece = (x % PPR) ^ flip(row);
+    static constexpr int FETCHES = BYTES / 1024;
+    // the i-th fetch of rows `bytes` apart
+    __device__ static __forceinline__ void fetch(gd_i4 r, int bytes, unsigned lds, int i, int lane) {
+        const int x = i * 64 + lane, row = x / PPR, piece = (x % PPR) ^ flip(row);
         gd_dma16(r, lds + i * 1024, row * bytes + piece * 16);
     }
     // row operand: rows of tile t, k block q
@@ -197,8 +246,8 @@ struct GdTile {
 
 // T or P.  In memory a row per token: for each part 64 columns, in the order of an operand's k slots (column
 // 32 b + 16 e + 4 g + r stands at 32 b + 8 g + 4 e + r; float32: as it is).  In LDS the operands
-// one after the other, those on and below the diagonal: 64 lanes' 16 bytes, a lane group's rows
-// exchanged by its number against bank conflicts of the transposed reads.
+// one after the other, those on and below the diagonal: 16 rows of 64 bytes, whose pieces are exchanged
+// by the row's number against bank conflicts.
 template <typename T, int PARTS>
 struct GdMat {
     typedef typename Mma<T>::Frag Frag;
@@ -207,11 +256,11 @@ struct GdMat {
     __device__ static __forceinline__ int tb(int t, int b) {  // of (row tile, k block)
         return TPK == 2 ? (t < 2 ? t : 2 * t - 2 + b) : t * (t + 1) / 2 + b;
     }
-    __device__ static __forceinline__ int slot(int lg, int lr) { return 16 * lg + (lr ^ (4 * lg)); }
-    static constexpr int FETCHES = (NTB * PARTS + 3) / 4;  // of each of four waves
-    static constexpr int ROW = D * (int)sizeof(T);         // bytes of a row in memory
-    __device__ static __forceinline__ void fetch(gd_i4 r, unsigned lds, int j, int wave, int lane) {
-        const int k = 4 * j + wave, i = k < NTB * PARTS ? k : NTB * PARTS - 1, x = i / PARTS, p = i % PARTS;
+    __device__ static __forceinline__ int slot(int lg, int lr) { return 4 * lr + (lg ^ (lr / 4)); }
+    static constexpr int FETCHES = NTB * PARTS;
+    static constexpr int ROW = D * (int)sizeof(T);  // bytes of a row in memory
+    __device__ static __forceinline__ void fetch(gd_i4 r, unsigned lds, int i, int lane) {
+        const int x = i / PARTS, p = i % PARTS;
         int t, b;
         if constexpr (TPK == 2) {
             t = x < 2 ? x : x / 2 + 1;
@@ -220,7 +269,8 @@ struct GdMat {
             t = x < 1 ? 0 : (x < 3 ? 1 : (x < 6 ? 2 : 3));
             b = x - t * (t + 1) / 2;
         }
-        const int lg = lane / 16, row = 16 * t + ((lane % 16) ^ (4 * lg));
+        // four lanes to 64 bytes of a row (sixteen rows' first pieces, then their second ones, .. take four times as long)
+        const int lr = lane / 4, lg = lane % 4 ^ (lr / 4), row = 16 * t + lr;
         gd_dma16(r, lds + i * 1024, row * ROW + 16 * lg + p * (GD_Q * (int)sizeof(T)) + 64 * b);
     }
     // row operand of tile t, columns of k block b
@@ -301,6 +351,20 @@ inline dim3 gd_grid(const GdArgs& a, int nblk) {
     return dim3((unsigned)((units + 7) / 8 * 8 * a.share * nblk));
 }
 
+// Waves of a walk's workgroup and column tiles of each.  Every wave reads all of a chunk's operands from LDS, at
+// 64 bytes a cycle for all waves of a CU: few waves to a CU where there are CUs left (a wave of 16 columns is
+// the least; the shard's 256 waves of 2 x 32 x 4 tiles take 467 us on 64 CUs), two tiles to a wave where there
+// are none.
+struct GdShape {
+    int waves, tiles;
+};
+inline GdShape gd_shape(const GdArgs& a) {
+    const int64_t tiles = (int64_t)a.nseq * a.H * (a.valdim / 16);
+    if (tiles <= 256) return {1, 1};
+    if (tiles <= 512) return {2, 1};
+    return {4, a.valdim / 64};
+}
+
 // Spans of one chunk each: numbers of chunks and places of the states that enter them.
 inline LaPlan gd_plan(const GdArgs& a) {
     LaPlan p;
@@ -316,10 +380,16 @@ inline LaPlan gd_plan(const GdArgs& a) {
 struct GdScalars {
     float in[GD_Q], out[GD_Q], beta[GD_Q];
 };
-__device__ __forceinline__ void gd_scalars_fetch(const GdArgs& a, int64_t row0, int n, unsigned lds, int wave, int lane) {
-    const int i = wave < 2 ? wave : 2;  // the last two waves bring the same
+__device__ __forceinline__ void gd_scalars_fetch(const GdArgs& a, int64_t row0, int n, unsigned lds, int i, int lane) {
     const float* p = i == 0 ? a.in : (i == 1 ? a.out : a.beta_of);
     gd_dma4(gd_rsrc(p + row0, n * 4), lds + i * GD_Q * 4, lane * 4);
 }
+// The number of the J-th fetch of a wave of NW, of N in all (the last ones may be fetched twice).
+template <int N, int NW>
+__device__ __forceinline__ int gd_mine(int j, int wave) {
+    const int i = j * NW + wave;
+    return N % NW == 0 || i < N ? i : N - 1;
+}
+constexpr int gd_share(int n, int waves) { return (n + waves - 1) / waves; }
 
 }  // namespace ssd

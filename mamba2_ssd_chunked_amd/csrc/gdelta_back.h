@@ -6,25 +6,25 @@
 
 namespace ssd {
 
-template <typename T, int BD, int CT, int PT>
+template <typename T, int BD, int CT, int NW, int PT>
 struct GdBackLds {
     static constexpr int k = 0, q = k + GdTile<T, BD>::BYTES, d = q + GdTile<T, BD>::BYTES,
-                         t = d + GdTile<T, 64 * CT>::BYTES, p = t + GdMat<T, PT>::BYTES,
+                         t = d + GdTile<T, 16 * CT * NW>::BYTES, p = t + GdMat<T, PT>::BYTES,
                          sc = p + GdMat<T, PT>::BYTES, bytes = (sc + (int)sizeof(GdScalars) + 1023) / 1024 * 1024;
     static constexpr int buffers = 2 * bytes <= 160 * 1024 ? 2 : 1;
 };
 
 // The gradient G of the state, as the forward walk keeps S: a wave owns columns of G^T.
-template <typename T, int BD, int CT, int PT>
-__global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
+template <typename T, int BD, int CT, int NW, int PT>
+__global__ void __launch_bounds__(64 * NW) k_gd_back(GdArgs a, LaPlan plan) {
     typedef Mma<T> M;
     typedef typename M::Frag Frag;
-    typedef GdBackLds<T, BD, CT, PT> L;
+    typedef GdBackLds<T, BD, CT, NW, PT> L;
     typedef GdTile<T, BD> Tile;
-    typedef GdTile<T, 64 * CT> TileV;
+    typedef GdTile<T, 16 * CT * NW> TileV;
     typedef GdMat<T, PT> Mat;
     constexpr int KS = M::KS, KB = BD / KS, TPK = LaCfg<T>::TPK, NK = GD_Q / KS;
-    constexpr int BT = BD / 16, CDW = 64 * CT;
+    constexpr int BT = BD / 16, CDW = 16 * CT * NW;
     __shared__ __align__(1024) char lds[L::buffers * L::bytes];
 
     const int nblk = a.valdim / CDW;
@@ -62,16 +62,17 @@ __global__ void __launch_bounds__(256) k_gd_back(GdArgs a, LaPlan plan) {
         x.p = gd_rsrc((const T*)a.P + x.row * Mat::D, x.n * Mat::ROW);
         return x;
     };
-    constexpr int NR = Tile::FETCHES, NM = Mat::FETCHES, NV = TileV::FETCHES, NF = 2 * NR + 2 * NM + NV + 1;
+    constexpr int FR = gd_share(Tile::FETCHES, NW), FM = gd_share(Mat::FETCHES, NW), FV = gd_share(TileV::FETCHES, NW);
+    constexpr int NF = 2 * FR + 2 * FM + FV + gd_share(3, NW);
     auto fetch = [&](const Next& x, auto I) {
-        constexpr int i = decltype(I)::value, at_d = NR, at_p = at_d + NV, at_t = at_p + NM, at_q = at_t + NM;
+        constexpr int i = decltype(I)::value, at_d = FR, at_p = at_d + FV, at_t = at_p + FM, at_q = at_t + FM, at_s = at_q + FR;
         const int es = (int)sizeof(T);
-        if constexpr (i < at_d) Tile::fetch(x.k, (int)a.k_ts * es, x.to + L::k, i, wave, lane);
-        else if constexpr (i < at_p) TileV::fetch(x.d, (int)a.o_ts * es, x.to + L::d, i - at_d, wave, lane);
-        else if constexpr (i < at_t) Mat::fetch(x.p, x.to + L::p, i - at_p, wave, lane);
-        else if constexpr (i < at_q) Mat::fetch(x.t, x.to + L::t, i - at_t, wave, lane);
-        else if constexpr (i < at_q + NR) Tile::fetch(x.q, (int)a.q_ts * es, x.to + L::q, i - at_q, wave, lane);
-        else gd_scalars_fetch(a, x.row, x.n, x.to + L::sc, wave, lane);
+        if constexpr (i < at_d) Tile::fetch(x.k, (int)a.k_ts * es, x.to + L::k, gd_mine<Tile::FETCHES, NW>(i, wave), lane);
+        else if constexpr (i < at_p) TileV::fetch(x.d, (int)a.o_ts * es, x.to + L::d, gd_mine<TileV::FETCHES, NW>(i - at_d, wave), lane);
+        else if constexpr (i < at_t) Mat::fetch(x.p, x.to + L::p, gd_mine<Mat::FETCHES, NW>(i - at_p, wave), lane);
+        else if constexpr (i < at_q) Mat::fetch(x.t, x.to + L::t, gd_mine<Mat::FETCHES, NW>(i - at_t, wave), lane);
+        else if constexpr (i < at_s) Tile::fetch(x.q, (int)a.q_ts * es, x.to + L::q, gd_mine<Tile::FETCHES, NW>(i - at_q, wave), lane);
+        else gd_scalars_fetch(a, x.row, x.n, x.to + L::sc, gd_mine<3, NW>(i - at_s, wave), lane);
     };
     auto stage_all = [&](int k) {
         const Next x = next_of(k, k);

@@ -2,6 +2,7 @@
 // gdelta_back.h.
 #include "gdelta_back.h"
 #include "gdelta_prep.h"
+#include "gdelta_team.h"
 #include "gdelta_walk.h"
 
 namespace ssd {
@@ -27,14 +28,25 @@ static GdBwdWs bwd_layout(const GdArgs& a, int act) {
 }
 size_t gd_bwd_ws(const GdArgs& a, int act) { return bwd_layout(a, act).total; }
 
+template <typename T, int DK, int CT, int NW>
+static hipError_t walks(const GdArgs& a, const LaPlan& p, hipStream_t s) {
+    constexpr int PT = sizeof(T) == 2 ? 3 : 1;
+    const dim3 grid = gd_grid(a, a.valdim / (16 * CT * NW)), block(64 * NW);
+    if (NW == 1) SSD_TRY(launch(k_gd_team<T, DK, PT, true>, grid, dim3(256), s, a, p));
+    else SSD_TRY(launch(k_gd_walk<T, DK, CT, NW, PT, true>, grid, block, s, a, p));
+    return launch(k_gd_back<T, DK, CT, NW, PT>, grid, block, s, a, p);
+}
+
 template <typename T, int DK, int DV>
 static hipError_t bwd_dims(const GdArgs& a, hipStream_t s) {
-    constexpr int PT = sizeof(T) == 2 ? 3 : 1, CT = 1;
+    constexpr int PT = sizeof(T) == 2 ? 3 : 1;
     const LaPlan p = gd_plan(a);
-    const dim3 walk = gd_grid(a, DV / (64 * CT));
+    const GdShape w = gd_shape(a);
     SSD_TRY(launch(k_gd_prep<T, DK, PT, PT, false>, dim3((unsigned)(p.slots * a.H)), dim3(256), s, a, p));
-    SSD_TRY(launch(k_gd_walk<T, DK, CT, PT, true>, walk, dim3(256), s, a, p));
-    SSD_TRY(launch(k_gd_back<T, DK, CT, PT>, walk, dim3(256), s, a, p));
+    if (w.waves == 1) SSD_TRY(walks<T, DK, 1, 1>(a, p, s));
+    else if (w.waves == 2) SSD_TRY(walks<T, DK, 1, 2>(a, p, s));
+    else if (DV == 64) SSD_TRY(walks<T, DK, 1, 4>(a, p, s));
+    else SSD_TRY(walks<T, DK, 2, 4>(a, p, s));
     return launch(k_gd_chunk<T, DK, DV>, dim3((unsigned)(p.slots * (a.H / a.share))), dim3(DK * 4), s, a, p);
 }
 

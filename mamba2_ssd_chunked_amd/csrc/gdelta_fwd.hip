@@ -1,5 +1,6 @@
 // The gated delta rule over prompts, forward: launches of gdelta_prep.h and gdelta_walk.h.
 #include "gdelta_prep.h"
+#include "gdelta_team.h"
 #include "gdelta_walk.h"
 
 namespace ssd {
@@ -19,18 +20,23 @@ static GdFwdWs fwd_layout(const GdArgs& a, int act) {
 }
 size_t gd_fwd_ws(const GdArgs& a, int act) { return fwd_layout(a, act).total; }
 
-template <typename T, int DK, int CT, int PT>
+template <typename T, int DK, int PT>
 static hipError_t fwd_parts(const GdArgs& a, hipStream_t s) {
     constexpr int PO = sizeof(T) == 2 ? 2 : 1;
     const LaPlan p = gd_plan(a);
+    const GdShape w = gd_shape(a);
     SSD_TRY(launch(k_gd_prep<T, DK, PT, PO, true>, dim3((unsigned)(p.slots * a.H)), dim3(256), s, a, p));
-    return launch(k_gd_walk<T, DK, CT, PT, false>, gd_grid(a, a.valdim / (64 * CT)), dim3(256), s, a, p);
+    const dim3 grid = gd_grid(a, a.valdim / (16 * w.waves * w.tiles));
+    if (w.waves == 1) return launch(k_gd_team<T, DK, PT, false>, grid, dim3(256), s, a, p);
+    if (w.waves == 2) return launch(k_gd_walk<T, DK, 1, 2, PT, false>, grid, dim3(128), s, a, p);
+    if (w.tiles == 1) return launch(k_gd_walk<T, DK, 1, 4, PT, false>, grid, dim3(256), s, a, p);
+    return launch(k_gd_walk<T, DK, 2, 4, PT, false>, grid, dim3(256), s, a, p);
 }
 
 template <typename T, int DK>
 static hipError_t fwd_dk(const GdArgs& a, hipStream_t s) {
-    if constexpr (sizeof(T) == 4) return fwd_parts<T, DK, 1, 1>(a, s);
-    else return a.fin ? fwd_parts<T, DK, 1, 3>(a, s) : fwd_parts<T, DK, 1, 2>(a, s);
+    if constexpr (sizeof(T) == 4) return fwd_parts<T, DK, 1>(a, s);
+    else return a.fin ? fwd_parts<T, DK, 3>(a, s) : fwd_parts<T, DK, 2>(a, s);
 }
 
 template <typename T>
