@@ -33,34 +33,27 @@ __device__ __forceinline__ float bn_gate(int kind, float z, float* d) {
     return z * s;
 }
 
-// The channels of thread `tid` of THR: EL in vectors of 8 (VEC) or one by one, neighbouring threads
+// The channels of thread `tid` of THR: EL in vectors of 4 (VEC) or one by one, neighbouring threads
 // side by side.
 template <int EL, bool VEC>
 struct BnMap {
     int tid, thr, C;
+    float inv;  // 1 / C
     __device__ __forceinline__ int channel(int e) const {
-        return VEC ? ((e / 8) * thr + tid) * 8 + e % 8 : e * thr + tid;
+        return VEC ? ((e / 4) * thr + tid) * 4 + e % 4 : e * thr + tid;
     }
     // 0 where there is no channel
     template <typename T>
     __device__ __forceinline__ void load(const T* p, float (&v)[EL]) const {
         if constexpr (VEC) {
             typedef typename Vec4<T>::type v4;
-            typedef T v8 __attribute__((ext_vector_type(8)));
 #pragma unroll
-            for (int e = 0; e < EL; e += 8) {
+            for (int e = 0; e < EL; e += 4) {
                 const int c = channel(e);
-                v8 x = {};
-                if (c < C) {
-                    if constexpr (sizeof(T) == 2) {
-                        x = *(const v8*)(p + c);
-                    } else {
-                        const v4 a = *(const v4*)(p + c), b = *(const v4*)(p + c + 4);
-                        x = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-                    }
-                }
+                v4 x = {};
+                if (c < C) x = *(const v4*)(p + c);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[e + i] = (float)x[i];
+                for (int i = 0; i < 4; ++i) v[e + i] = (float)x[i];
             }
         } else {
 #pragma unroll
@@ -79,21 +72,10 @@ struct BnMap {
     __device__ __forceinline__ void store(T* p, const float (&v)[EL]) const {
         if constexpr (VEC) {
             typedef typename Vec4<T>::type v4;
-            typedef T v8 __attribute__((ext_vector_type(8)));
 #pragma unroll
-            for (int e = 0; e < EL; e += 8) {
-                const int c = channel(e);
-                if (c >= C) continue;
-                v8 x;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = (T)v[e + i];
-                if constexpr (sizeof(T) == 2) {
-                    *(v8*)(p + c) = x;
-                } else {
-                    *(v4*)(p + c) = __builtin_shufflevector(x, x, 0, 1, 2, 3);
-                    *(v4*)(p + c + 4) = __builtin_shufflevector(x, x, 4, 5, 6, 7);
-                }
-            }
+            for (int e = 0; e < EL; e += 4)
+                if (channel(e) < C)
+                    *(v4*)(p + channel(e)) = v4{(T)v[e], (T)v[e + 1], (T)v[e + 2], (T)v[e + 3]};
         } else {
 #pragma unroll
             for (int e = 0; e < EL; ++e)
@@ -102,41 +84,60 @@ struct BnMap {
     }
 };
 
-// Sums of a and b over the workgroup, the same for all threads.
-__device__ __forceinline__ void bn_sum2(float& a, float& b, float* red) {
+// Sum over the wave, the same for all lanes, without a trip through LDS.
+__device__ __forceinline__ float bn_wave_sum(float v) {
+    auto dpp = [](float x, auto ctrl) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    v += dpp(v, std::integral_constant<int, 0xb1>{});   // lanes 1 0 3 2 of four
+    v += dpp(v, std::integral_constant<int, 0x4e>{});   // 2 3 0 1
+    v += dpp(v, std::integral_constant<int, 0x141>{});  // eight mirrored
+    v += dpp(v, std::integral_constant<int, 0x140>{});  // sixteen mirrored
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
+// Sums over the workgroup, the same for all threads.
+template <int N>
+__device__ __forceinline__ void bn_sum(float (&v)[N], float (*red)[16]) {
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        a += __shfl_xor(a, o, 64);
-        b += __shfl_xor(b, o, 64);
-    }
+    for (int i = 0; i < N; ++i) v[i] = bn_wave_sum(v[i]);
     const int waves = blockDim.x / 64;
     if (waves == 1) return;
     __syncthreads();  // the last sums are read
-    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = a, red[8 + threadIdx.x / 64] = b;
+    if (threadIdx.x % 64 == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[i][threadIdx.x / 64] = v[i];
     __syncthreads();
-    a = b = 0.f;
-    for (int w = 0; w < waves; ++w) a += red[w], b += red[8 + w];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const f32x4* r = (const f32x4*)red[i];
+        f32x4 s = r[0];
+        for (int w = 4; w < waves; w += 4) s += r[w / 4];  // zeros behind the last wave
+        v[i] = (s[0] + s[1]) + (s[2] + s[3]);
+    }
 }
 
 // n = norm(v) in place of v; returns 1 / deviation.  Channels beyond C stay 0.
 template <int EL, bool VEC>
 __device__ __forceinline__ float bn_norm(const BnMap<EL, VEC>& m, float (&v)[EL], int center, float eps,
-                                         float* red) {
-    const float inv = 1.f / (float)m.C;
-    float s = 0.f, q = 0.f, none = 0.f;
+                                         float (*red)[16]) {
     if (center) {
+        float s[1] = {0.f};
 #pragma unroll
-        for (int e = 0; e < EL; ++e) s += v[e];
-        bn_sum2(s, none, red);
-        s *= inv;
+        for (int e = 0; e < EL; ++e) s[0] += v[e];
+        bn_sum(s, red);
+        s[0] *= m.inv;
 #pragma unroll
-        for (int e = 0; e < EL; ++e) v[e] = m.channel(e) < m.C ? v[e] - s : 0.f;
+        for (int e = 0; e < EL; ++e) v[e] = m.channel(e) < m.C ? v[e] - s[0] : 0.f;
     }
-    none = 0.f;
+    float q[1] = {0.f};
 #pragma unroll
-    for (int e = 0; e < EL; ++e) q += v[e] * v[e];
-    bn_sum2(q, none, red);
-    const float rstd = 1.f / sqrtf(q * inv + eps);
+    for (int e = 0; e < EL; ++e) q[0] += v[e] * v[e];
+    bn_sum(q, red);
+    const float rstd = 1.f / sqrtf(q[0] * m.inv + eps);
 #pragma unroll
     for (int e = 0; e < EL; ++e) v[e] *= rstd;
     return rstd;
@@ -145,22 +146,28 @@ __device__ __forceinline__ float bn_norm(const BnMap<EL, VEC>& m, float (&v)[EL]
 // Gradient of norm's input from that of its output, in place.
 template <int EL, bool VEC>
 __device__ __forceinline__ void bn_back(const BnMap<EL, VEC>& m, float (&g)[EL], const float (&n)[EL],
-                                        float rstd, int center, float* red) {
-    const float inv = 1.f / (float)m.C;
-    float s = 0.f, q = 0.f;
+                                        float rstd, int center, float (*red)[16]) {
+    float s[2] = {0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < EL; ++e) s += g[e], q += g[e] * n[e];
-    bn_sum2(s, q, red);
-    s = center ? s * inv : 0.f;
-    q *= inv;
+    for (int e = 0; e < EL; ++e) s[0] += g[e] * n[e], s[1] += g[e];
+    if (center) {
+        bn_sum(s, red);
+    } else {
+        float q[1] = {s[0]};
+        bn_sum(q, red);
+        s[0] = q[0], s[1] = 0.f;
+    }
+    s[0] *= m.inv, s[1] *= m.inv;
 #pragma unroll
-    for (int e = 0; e < EL; ++e) g[e] = rstd * (g[e] - s - n[e] * q);
+    for (int e = 0; e < EL; ++e) g[e] = rstd * (g[e] - s[1] - n[e] * s[0]);
 }
 
 template <typename T, typename R, int EL, bool VEC>
-__global__ void __launch_bounds__(512) k_block_fwd(BlockArgs a) {
-    __shared__ float red[16];
-    const BnMap<EL, VEC> m = {(int)threadIdx.x, (int)blockDim.x, a.C};
+__global__ void __launch_bounds__(1024) k_block_fwd(BlockArgs a) {
+    __shared__ __align__(16) float red[2][16];
+    if (threadIdx.x < 32) red[threadIdx.x / 16][threadIdx.x % 16] = 0.f;
+    __syncthreads();
+    const BnMap<EL, VEC> m = {(int)threadIdx.x, (int)blockDim.x, a.C, 1.f / (float)a.C};
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         float u[EL], v[EL], w[EL];
         m.load((const T*)a.y + row * a.ys, u);
@@ -202,9 +209,11 @@ __global__ void __launch_bounds__(512) k_block_fwd(BlockArgs a) {
 
 // part: [workgroup][5][C] sums of dscale, dw1, db1, dw2, db2.
 template <typename T, typename R, int EL, bool VEC>
-__global__ void __launch_bounds__(512) k_block_bwd(BlockArgs a, float* __restrict__ part) {
-    __shared__ float red[16];
-    const BnMap<EL, VEC> m = {(int)threadIdx.x, (int)blockDim.x, a.C};
+__global__ void __launch_bounds__(1024) k_block_bwd(BlockArgs a, float* __restrict__ part) {
+    __shared__ __align__(16) float red[2][16];
+    if (threadIdx.x < 32) red[threadIdx.x / 16][threadIdx.x % 16] = 0.f;
+    __syncthreads();
+    const BnMap<EL, VEC> m = {(int)threadIdx.x, (int)blockDim.x, a.C, 1.f / (float)a.C};
     float ds[EL], dw1[EL], db1[EL], dw2[EL], db2[EL];
 #pragma unroll
     for (int e = 0; e < EL; ++e) ds[e] = dw1[e] = db1[e] = dw2[e] = db2[e] = 0.f;
@@ -236,12 +245,18 @@ __global__ void __launch_bounds__(512) k_block_bwd(BlockArgs a, float* __restric
             for (int e = 0; e < EL; ++e) u[e] = n[e];
         }
         m.load_or(a.scale, 1.f, s);
+        float f[EL];  // act(z); z becomes its derivative times u
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+            float d = 0.f;
+            f[e] = 1.f;
+            if (a.gate) f[e] = bn_gate(a.gate, z[e], &d);
+            z[e] = d * u[e];
+            u[e] *= f[e];
+        }
         if (a.pre) {
 #pragma unroll
-            for (int e = 0; e < EL; ++e) {
-                const float f = a.gate ? bn_gate(a.gate, z[e], nullptr) : 1.f;
-                v[e] = a.alpha * v[e] + s[e] * (u[e] * f);
-            }
+            for (int e = 0; e < EL; ++e) v[e] = a.alpha * v[e] + s[e] * u[e];
             const float rstd = bn_norm(m, v, a.center, a.eps, red);
 #pragma unroll
             for (int e = 0; e < EL; ++e) dw2[e] += t[e] * v[e], db2[e] += t[e];
@@ -258,12 +273,10 @@ __global__ void __launch_bounds__(512) k_block_bwd(BlockArgs a, float* __restric
         m.store((R*)a.dx + row * a.dxs, t);
 #pragma unroll
         for (int e = 0; e < EL; ++e) {
-            float f = 1.f, d = 0.f;
-            if (a.gate) f = bn_gate(a.gate, z[e], &d);
-            ds[e] += G[e] * (u[e] * f);
+            ds[e] += G[e] * u[e];
             const float dm = s[e] * G[e];
-            z[e] = dm * u[e] * d;
-            t[e] = dm * f;
+            z[e] *= dm;
+            t[e] = dm * f[e];
         }
         if (a.gate) m.store((T*)a.dz + row * a.dzs, z);
         if (a.post) {
@@ -290,37 +303,49 @@ __global__ void __launch_bounds__(512) k_block_bwd(BlockArgs a, float* __restric
         }
 }
 
-// Adds up `n` workgroups' sums: 64 columns to a workgroup, its four waves a quarter of them each.
+// Adds up `n` workgroups' sums: 16 columns to a workgroup, whose 16 groups of lanes take every 16th of them
+// (64 columns, a quarter of the sums to a wave: 81 us for 1024 of 5 x 2048).
 __global__ void __launch_bounds__(256) k_block_sums(BlockArgs a, const float* __restrict__ part, int n) {
-    __shared__ float red[4][64];
-    const int w = threadIdx.x / 64, lane = threadIdx.x % 64, all = 5 * a.C;
-    const int c = blockIdx.x * 64 + lane;
-    float s = 0.f;
-    if (c < all) {
-        const int q = (n + 3) / 4, end = (w + 1) * q < n ? (w + 1) * q : n;
-        for (int i = w * q; i < end; ++i) s += part[(int64_t)i * all + c];
-    }
-    red[w][lane] = s;
+    __shared__ float red[16][17];
+    const int g = threadIdx.x / 16, lane = threadIdx.x % 16, all = 5 * a.C;
+    const int c = blockIdx.x * 16 + lane;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (c < all)
+        for (int i = g; i < n; i += 128)
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (i + 16 * u < n) s[u] += part[(int64_t)(i + 16 * u) * all + c];
+    red[g][lane] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     __syncthreads();
-    if (w == 0 && c < all) {
+    if (g == 0 && c < all) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v += red[i][lane];
         float* const out[5] = {a.dscale, a.dw1, a.db1, a.dw2, a.db2};
         float* p = c / a.C == 0 ? out[0] : (c / a.C == 1 ? out[1] : (c / a.C == 2 ? out[2] : (c / a.C == 3 ? out[3] : out[4])));
-        if (p) p[c % a.C] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+        if (p) p[c % a.C] = v;
     }
 }
 
-// Workgroups of the backward: enough to fill the CUs four times over, and few enough that their sums
-// are a small part of the traffic.
-static int bwd_blocks(const BlockArgs& a) { return (int)(a.rows < 1024 ? a.rows : 1024); }
+static int block_threads(int C) {  // 4 channels to each, 8 or 16 where 1024 are not enough
+    const int t = (C + 255) / 256 * 64;
+    return t <= 1024 ? t : (t <= 2048 ? (t / 2 + 63) / 64 * 64 : 1024);
+}
+// Workgroups of the backward: as many as the CUs hold at once (1024 threads each), so that their sums are a
+// small part of the traffic.
+static int bwd_blocks(const BlockArgs& a) {
+    const int64_t n = 256 * 1024 / block_threads(a.C);
+    return (int)(a.rows < n ? a.rows : n);
+}
 size_t block_bwd_ws(const BlockArgs& a) { return align256((size_t)bwd_blocks(a) * 5 * a.C * 4); }
 
-// Whether all rows can be read and written in vectors of 8 channels.
+// Whether all rows can be read and written in vectors of 4 channels.
 static bool vectors(const BlockArgs& a, int act, int res) {
     auto ok = [](const void* p, int64_t stride, int esz) {
-        return !p || (((uintptr_t)p | (uintptr_t)(stride * esz)) & 15) == 0;
+        return !p || (((uintptr_t)p | (uintptr_t)(stride * esz)) & (4 * esz - 1)) == 0;
     };
     const int e = act == SSD_BF16 ? 2 : 4, f = res == SSD_BF16 ? 2 : 4;
-    if (a.C % 8 != 0) return false;
+    if (a.C % 4 != 0) return false;
     for (const float* p : {a.scale, a.w1, a.b1, a.w2, a.b2})
         if (!ok(p, 0, 4)) return false;
     return ok(a.x, a.xs, f) && ok(a.y, a.ys, e) && ok(a.z, a.zs, e) && ok(a.r, a.rs, f) && ok(a.dr, a.rs, f) &&
@@ -335,16 +360,17 @@ static hipError_t go(const BlockArgs& a, float* part, int threads, hipStream_t s
     }
     const int n = bwd_blocks(a);
     SSD_TRY(launch(k_block_bwd<T, R, EL, VEC>, dim3(n), dim3(threads), s, a, part));
-    return launch(k_block_sums, dim3((5 * a.C + 63) / 64), dim3(256), s, a, part, n);
+    return launch(k_block_sums, dim3((5 * a.C + 15) / 16), dim3(256), s, a, part, n);
 }
 
-// 8 channels to a thread up to 512 threads, then 16 and 32.
+// (8 channels to a thread from the start take 128 registers and more in the backward: 300 us for 16384 rows
+// of 2048, 255 with 4.)
 template <typename T, typename R, bool VEC>
 static hipError_t width(const BlockArgs& a, float* part, hipStream_t s) {
-    const int threads = (a.C + 511) / 512 * 64;
-    if (threads <= 512) return go<T, R, 8, VEC>(a, part, threads, s);
-    if (threads <= 1024) return go<T, R, 16, VEC>(a, part, 512, s);
-    return go<T, R, 32, VEC>(a, part, 512, s);
+    const int threads = block_threads(a.C);
+    if (a.C <= 4 * threads) return go<T, R, 4, VEC>(a, part, threads, s);
+    if (a.C <= 8 * threads) return go<T, R, 8, VEC>(a, part, threads, s);
+    return go<T, R, 16, VEC>(a, part, threads, s);
 }
 static hipError_t types(const BlockArgs& a, int act, int res, float* part, hipStream_t s) {
     const bool v = vectors(a, act, res);

@@ -289,21 +289,6 @@ struct GdChunkLds {
     static constexpr int bytes = rows * (int)sizeof(T);
 };
 
-// Eight neighbouring elements as float32.
-template <typename T>
-__device__ __forceinline__ void gd_eight(const T* p, float (&v)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        const bf16x8 x = *(const bf16x8*)p;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (float)x[e];
-    } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[4 * e + r] = (float)p[4 * e + r];
-    }
-}
-
 // Gradients of one chunk of the heads that share a key head.  A wave owns 16 key channels: dq^T and dk^T
 // [bd][token], summed over the heads in registers, in their order.
 template <typename T, int DK, int DV>
@@ -335,13 +320,9 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
     const int n = sp.n, wave = wave_id(), lane = threadIdx.x % 64, lr = lane % 16, lg = lane / 16;
     const int64_t t0 = sp.lo + sp.i0;
     const int b0 = 16 * wave;
-    {
-        GdRows<T, DK, NTHR> r;
-        r.load((const T*)a.k + (int64_t)hk * DK, a.k_ts, t0, n);
-        r.store(sk);
-        r.load((const T*)a.q + (int64_t)hk * DK, a.q_ts, t0, n);
-        r.store(sq);
-    }
+    GdRows<T, DK, NTHR> rk, rq;
+    rk.load((const T*)a.k + (int64_t)hk * DK, a.k_ts, t0, n);
+    rq.load((const T*)a.q + (int64_t)hk * DK, a.q_ts, t0, n);
     f32x4 DQ[GD_NT], DKt[GD_NT];
 #pragma unroll
     for (int t = 0; t < GD_NT; ++t) DQ[t] = DKt[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -350,59 +331,98 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
         const int h = hk * a.share + m;
         const int64_t row0 = (int64_t)h * a.tokens + t0;
         if (m > 0) __syncthreads();  // the last head's reads are done
-        if (threadIdx.x < GD_Q) {
-            const bool live = threadIdx.x < n;
-            s_in[threadIdx.x] = live ? a.in[row0 + threadIdx.x] : 0.f;
-            s_out[threadIdx.x] = live ? a.out[row0 + threadIdx.x] : 0.f;
-            s_beta[threadIdx.x] = live ? a.beta_of[row0 + threadIdx.x] : 1.f;
-            c2[threadIdx.x] = live ? a.c2[row0 + threadIdx.x] : -1e30;  // no factor of a row without a token
-        }
-        const T* pd = (const T*)a.dout + t0 * a.o_ts + (int64_t)h * DV;
-        if constexpr (L::DO) {
-            GdRows<T, DV, NTHR> r;
-            r.load((const T*)a.dout + (int64_t)h * DV, a.o_ts, t0, n);
-            r.store(sd);
-        }
-        // U and Z in parts; dv, dbeta and v . dv from them
+        // All that a head reads is asked for at once, but for G: one wait where each piece would have its own
+        // (8192 chunks of 128 x 128: 930 us, 885 so; 23 chunks of 64 x 64: 49, 41).
+        typedef T t4 __attribute__((ext_vector_type(4)));
+        constexpr int VPR = DV / 8, NX = GD_Q * VPR / NTHR;  // runs of eight value channels of a row, of a thread
+        static_assert(GD_Q * VPR % NTHR == 0, "the threads tile the rows");
         const __amdgpu_buffer_rsrc_t ru = buf_rsrc(a.U + row0 * DV, n * DV * 4), rz = buf_rsrc(a.Z + row0 * DV, n * DV * 4);
-        constexpr int VPR = DV / 8;
+        const __amdgpu_buffer_rsrc_t rv = buf_rsrc((const T*)a.v + t0 * a.v_ts + (int64_t)h * DV, n * (int)a.v_ts * (int)sizeof(T));
+        const T* pd = (const T*)a.dout + t0 * a.o_ts + (int64_t)h * DV;
+        const bool live = threadIdx.x < n;
+        const float rin = live ? a.in[row0 + threadIdx.x] : 0.f, rout = live ? a.out[row0 + threadIdx.x] : 0.f;
+        const float rbeta = live ? a.beta_of[row0 + threadIdx.x] : 1.f;
+        const double rc = live ? a.c2[row0 + threadIdx.x] : -1e30;  // no factor of a row without a token
+        GdRows<T, DV, NTHR> rd;
+        if constexpr (L::DO) rd.load((const T*)a.dout + (int64_t)h * DV, a.o_ts, t0, n);
+        f32x4 u[NX][2], z[NX][2];
+        t4 vv[NX][2];
+        float be[NX];
 #pragma unroll
-        for (int x = threadIdx.x; x < GD_Q * VPR; x += NTHR) {
-            const int row = x / VPR, c = x % VPR * 8;
-            f32x4 u[2], z[2];
+        for (int i = 0; i < NX; ++i) {
+            const int y = i * NTHR + threadIdx.x, row = y / VPR, c = y % VPR * 8;
+            be[i] = row < n ? a.beta_of[row0 + row] : 1.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                u[e] = buf_load<f32x4>(ru, (row * DV + c + 4 * e) * 4);
-                z[e] = buf_load<f32x4>(rz, (row * DV + c + 4 * e) * 4);
+                u[i][e] = buf_load<f32x4>(ru, (row * DV + c + 4 * e) * 4);
+                z[i][e] = buf_load<f32x4>(rz, (row * DV + c + 4 * e) * 4);
+                vv[i][e] = buf_load<t4>(rv, (row * (int)a.v_ts + c + 4 * e) * (int)sizeof(T));
             }
-            const int live = row < n;
-            const float be = live ? a.beta_of[row0 + row] : 1.f;
-            float v[8], dv[8], zu = 0.f, vz = 0.f;
-            gd_eight((const T*)a.v + (t0 + (live ? row : 0)) * a.v_ts + (int64_t)h * DV + c, v);
+        }
+        // S and G of this wave's key channels: a lane has channel b0 + lr and value channels in k order
+        const int64_t state = ((int64_t)sp.s * a.H + h) * ((int64_t)DK * DV);
+        const float *pS = nullptr, *pG = nullptr;  // kept ones: [bd][cd]
+        if (sp.i0 > 0) pS = a.S + (la_place(a, plan, sp.s, sp.lo, sp.j) * a.H + h) * ((int64_t)DK * DV);
+        if (!sp.last) pG = a.G + (la_place(a, plan, sp.s, sp.lo, sp.j + 1) * a.H + h) * ((int64_t)DK * DV);
+        auto channels = [&](const float* kept, const float* given, int q, f32x4 (&v)[TPK]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                zu += z[e / 4][e % 4] * u[e / 4][e % 4];
-                dv[e] = be * z[e / 4][e % 4];
-                if (live) vz += dv[e] * v[e];
+            for (int e = 0; e < TPK; ++e) {
+                const int c = KS * q + SL * lg + 4 * e;
+                if (kept) {
+                    v[e] = *(const f32x4*)(kept + (b0 + lr) * DV + c);
+                } else if (given) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[e][r] = given[state + (int64_t)(c + r) * DK + b0 + lr];
+                } else {
+                    v[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+            }
+        };
+        f32x4 s[KV][TPK];
+#pragma unroll
+        for (int q = 0; q < KV; ++q) channels(pS, a.init, q, s[q]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (m == 0) {
+            rk.store(sk);
+            rq.store(sq);
+        }
+        if (threadIdx.x < GD_Q) {
+            s_in[threadIdx.x] = rin;
+            s_out[threadIdx.x] = rout;
+            s_beta[threadIdx.x] = rbeta;
+            c2[threadIdx.x] = rc;
+        }
+        if constexpr (L::DO) rd.store(sd);
+        // U and Z in parts; dv, dbeta and v . dv from them
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int y = i * NTHR + threadIdx.x, row = y / VPR, c = y % VPR * 8;
+            float zu = 0.f, vz = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                t4 o;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    zu += z[i][e][r] * u[i][e][r];
+                    const float dv = be[i] * z[i][e][r];
+                    vz += dv * (float)vv[i][e][r];
+                    o[r] = (T)dv;
+                }
+                if (row < n) *(t4*)((T*)a.dv + (t0 + row) * a.dv_ts + (int64_t)h * DV + c + 4 * e) = o;
             }
 #pragma unroll
             for (int o = 1; o < VPR; o <<= 1) {
                 zu += __shfl_xor(zu, o, 64);
                 vz += __shfl_xor(vz, o, 64);
             }
-            if (x % VPR == 0) zv[row] = vz;
-            if (live) {
-                if (x % VPR == 0) a.dbeta[(t0 + row) * a.H + h] = zu / be;
-                T* p = (T*)a.dv + (t0 + row) * a.dv_ts + (int64_t)h * DV + c;
-                typedef T t4 __attribute__((ext_vector_type(4)));
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *(t4*)(p + 4 * e) = t4{(T)dv[4 * e], (T)dv[4 * e + 1], (T)dv[4 * e + 2], (T)dv[4 * e + 3]};
+            if (y % VPR == 0) {
+                zv[row] = vz;
+                if (row < n) a.dbeta[(t0 + row) * a.H + h] = zu / be[i];
             }
             if constexpr (sizeof(T) == 2) {
                 Frag f[P::U], g[P::Z];
-                gd_split<T, P::U>(u, f);
-                gd_split<T, P::Z>(z, g);
+                gd_split<T, P::U>(u[i], f);
+                gd_split<T, P::Z>(z[i], g);
 #pragma unroll
                 for (int p = 0; p < P::U; ++p) *(Frag*)(su + (p * GD_Q + row) * VP + c) = f[p];
 #pragma unroll
@@ -410,11 +430,15 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
             } else {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    *(f32x4*)(su + row * VP + c + 4 * e) = u[e];
-                    *(f32x4*)(sz + row * VP + c + 4 * e) = z[e];
+                    *(f32x4*)(su + row * VP + c + 4 * e) = u[i][e];
+                    *(f32x4*)(sz + row * VP + c + 4 * e) = z[i][e];
                 }
             }
         }
+        f32x4 g[KV][TPK];
+#pragma unroll
+        for (int q = 0; q < KV; ++q) channels(pG, a.dfin, q, g[q]);
+        __builtin_amdgcn_sched_barrier(0);
         __syncthreads();
 
         // k operands of value channels: rows of do, U, Z
@@ -463,41 +487,19 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
             }
         }
 
-        // S and G of this wave's key channels: a lane has channel b0 + lr and value channels in k order
         f32x4 dq[GD_NT], gu[GD_NT], sz_[GD_NT];
 #pragma unroll
         for (int t = 0; t < GD_NT; ++t) dq[t] = gu[t] = sz_[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         float dot = 0.f;
-        const int64_t state = ((int64_t)sp.s * a.H + h) * ((int64_t)DK * DV);
-        const float *pS = nullptr, *pG = nullptr;  // kept ones: [bd][cd]
-        if (sp.i0 > 0) pS = a.S + (la_place(a, plan, sp.s, sp.lo, sp.j) * a.H + h) * ((int64_t)DK * DV);
-        if (!sp.last) pG = a.G + (la_place(a, plan, sp.s, sp.lo, sp.j + 1) * a.H + h) * ((int64_t)DK * DV);
-        auto channels = [&](const float* kept, const float* given, int q, f32x4 (&v)[TPK]) {
-#pragma unroll
-            for (int e = 0; e < TPK; ++e) {
-                const int c = KS * q + SL * lg + 4 * e;
-                if (kept) {
-                    v[e] = *(const f32x4*)(kept + (b0 + lr) * DV + c);
-                } else if (given) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) v[e][r] = given[state + (int64_t)(c + r) * DK + b0 + lr];
-                } else {
-                    v[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
-            }
-        };
 #pragma unroll
         for (int q = 0; q < KV; ++q) {
-            f32x4 s[TPK], g[TPK];
-            channels(pS, a.init, q, s);
-            channels(pG, a.dfin, q, g);
 #pragma unroll
             for (int e = 0; e < TPK; ++e)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) dot += s[e][r] * g[e][r];
+                for (int r = 0; r < 4; ++r) dot += s[q][e][r] * g[q][e][r];
             Frag sf[P::U], gf[P::U];
-            gd_split<T, P::U>(s, sf);
-            gd_split<T, P::U>(g, gf);
+            gd_split<T, P::U>(s[q], sf);
+            gd_split<T, P::U>(g[q], gf);
 #pragma unroll
             for (int t = 0; t < GD_NT; ++t) {
                 Frag uf[P::U], zf[P::Z];
@@ -510,10 +512,10 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
                 gu[t] = gd_mma<T, P::U, P::U>(gf, uf, gu[t]);
                 sz_[t] = gd_mma<T, P::Z, P::Z>(sf, zf, sz_[t]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         // <G, S behind> = e^C <G, S> + sum_j e^(C - c_j) k_j . (G u_j)
         dot *= s_in[n - 1];
-        typedef T t4 __attribute__((ext_vector_type(4)));
 #pragma unroll
         for (int t = 0; t < GD_NT; ++t) {
             const int i = 16 * t + lr;
