@@ -42,6 +42,25 @@ struct BnMap {
     __device__ __forceinline__ int channel(int e) const {
         return VEC ? ((e / 4) * thr + tid) * 4 + e % 4 : e * thr + tid;
     }
+    // a load in two steps: the raw values on their way, then as float32
+    template <typename T>
+    struct Raw {
+        typename Vec4<T>::type v[VEC ? EL / 4 : 1];
+    };
+    template <typename T>
+    __device__ __forceinline__ void ask(const T* p, Raw<T>& r) const {
+#pragma unroll
+        for (int e = 0; e < EL; e += 4) {
+            typename Vec4<T>::type x = {};
+            if (channel(e) < C) x = *(const typename Vec4<T>::type*)(p + channel(e));
+            r.v[e / 4] = x;
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void take(const Raw<T>& r, float (&v)[EL]) const {
+#pragma unroll
+        for (int e = 0; e < EL; ++e) v[e] = (float)r.v[e / 4][e % 4];
+    }
     // 0 where there is no channel
     template <typename T>
     __device__ __forceinline__ void load(const T* p, float (&v)[EL]) const {
@@ -217,18 +236,38 @@ __global__ void __launch_bounds__(1024) k_block_bwd(BlockArgs a, float* __restri
     float ds[EL], dw1[EL], db1[EL], dw2[EL], db2[EL];
 #pragma unroll
     for (int e = 0; e < EL; ++e) ds[e] = dw1[e] = db1[e] = dw2[e] = db2[e] = 0.f;
+    // Where registers allow, the next row is on its way while one is computed.
+    constexpr bool AHEAD = VEC && EL == 4;
+    typename BnMap<EL, VEC>::template Raw<T> ry, rz, rh;
+    typename BnMap<EL, VEC>::template Raw<R> rx, rr;
+    auto ask = [&](int64_t row) {
+        if constexpr (AHEAD) {
+            m.ask((const T*)a.y + row * a.ys, ry);
+            m.ask((const R*)a.x + row * a.xs, rx);
+            if (a.gate) m.ask((const T*)a.z + row * a.zs, rz);
+            if (a.dr) m.ask((const R*)a.dr + row * a.rs, rr);
+            if (a.pre) m.ask((const T*)a.dh + row * a.hs, rh);
+        }
+    };
+    ask(blockIdx.x);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         float n[EL], u[EL], z[EL], v[EL], G[EL], s[EL], t[EL];
-        m.load((const T*)a.y + row * a.ys, n);
-        m.load((const R*)a.x + row * a.xs, v);
-        if (a.gate) m.load((const T*)a.z + row * a.zs, z);
-        if (a.dr) {
-            m.load((const R*)a.dr + row * a.rs, G);
-        } else {
 #pragma unroll
-            for (int e = 0; e < EL; ++e) G[e] = 0.f;
+        for (int e = 0; e < EL; ++e) G[e] = 0.f;
+        if constexpr (AHEAD) {
+            m.take(ry, n);
+            m.take(rx, v);
+            if (a.gate) m.take(rz, z);
+            if (a.dr) m.take(rr, G);
+            if (a.pre) m.take(rh, t);
+            ask(row + gridDim.x < a.rows ? row + gridDim.x : row);  // the last row again: nobody takes it
+        } else {
+            m.load((const T*)a.y + row * a.ys, n);
+            m.load((const R*)a.x + row * a.xs, v);
+            if (a.gate) m.load((const T*)a.z + row * a.zs, z);
+            if (a.dr) m.load((const R*)a.dr + row * a.rs, G);
+            if (a.pre) m.load((const T*)a.dh + row * a.hs, t);
         }
-        if (a.pre) m.load((const T*)a.dh + row * a.hs, t);
         float rstd1 = 0.f;
         if (a.post) {
             rstd1 = bn_norm(m, n, a.center, a.eps, red);
