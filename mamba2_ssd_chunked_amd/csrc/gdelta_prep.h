@@ -22,8 +22,11 @@ __global__ void __launch_bounds__(256) k_gd_prep(GdArgs a, LaPlan plan) {
     typedef Mma<T> M;
     typedef typename M::Frag Frag;
     constexpr int SL = M::SL, KS = M::KS, KB = DK / KS, AP = GdRows<T, DK>::PITCH, FP = GD_Q + 4;
-    __shared__ __align__(16) T sk[GD_Q * AP], sq[GD_Q * AP];
-    __shared__ __align__(16) float A[GD_Q * FP];
+    constexpr int QB = GD_Q * AP * (int)sizeof(T), AB = GD_Q * FP * 4;
+    __shared__ __align__(16) T sk[GD_Q * AP];
+    __shared__ __align__(16) char both[QB > AB ? QB : AB];  // the queries, then A (four workgroups fit a CU)
+    T* sq = (T*)both;
+    float* A = (float*)both;
     __shared__ double c2[GD_Q];  // c in units of log 2
     __shared__ float sbeta[GD_Q];
     __shared__ int sbad;
@@ -89,6 +92,7 @@ __global__ void __launch_bounds__(256) k_gd_prep(GdArgs a, LaPlan plan) {
             kf[q] = M::load(sk + i * AP + KS * q + SL * lg);
             qf[q] = M::load(sq + i * AP + KS * q + SL * lg);
         }
+        __syncthreads();  // the queries are read
         const double ci = c2[i];
         const float bi = sbeta[i];
         const __amdgpu_buffer_rsrc_t rp = buf_rsrc((T*)a.P + row0 * (GD_Q * PP), n * GD_Q * PP * (int)sizeof(T));
