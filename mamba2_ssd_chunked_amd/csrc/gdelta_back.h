@@ -314,8 +314,10 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
     T* se = su;
     T* sn = se + GD_Q * L::EP;
 
-    const int groups = a.H / a.share, hk = blockIdx.x % groups;
-    const LaSpan sp = la_span(a, plan, blockIdx.x / groups);
+    // a workgroup takes the heads of a key head in turn, or (a.sums) one head, whose dq and dk it leaves in float32
+    const int heads = a.sums ? 1 : a.share, items = a.H / heads;
+    const int h0 = (int)(blockIdx.x % items) * heads, hk = h0 / a.share;
+    const LaSpan sp = la_span(a, plan, blockIdx.x / items);
     if (sp.s < 0 || sp.n <= 0) return;
     const int n = sp.n, wave = wave_id(), lane = threadIdx.x % 64, lr = lane % 16, lg = lane / 16;
     const int64_t t0 = sp.lo + sp.i0;
@@ -327,8 +329,8 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
 #pragma unroll
     for (int t = 0; t < GD_NT; ++t) DQ[t] = DKt[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    for (int m = 0; m < a.share; ++m) {
-        const int h = hk * a.share + m;
+    for (int m = 0; m < heads; ++m) {
+        const int h = h0 + m;
         const int64_t row0 = (int64_t)h * a.tokens + t0;
         if (m > 0) __syncthreads();  // the last head's reads are done
         // All that a head reads is asked for at once, but for G: one wait where each piece would have its own
@@ -612,6 +614,15 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
         }
     }
 
+    if (a.sums) {
+        const __amdgpu_buffer_rsrc_t r = buf_rsrc(a.sums + ((int64_t)h0 * a.tokens + t0) * (2 * DK), n * 2 * DK * 4);
+#pragma unroll
+        for (int t = 0; t < GD_NT; ++t) {
+            buf_store(DQ[t], r, ((16 * t + lr) * 2 * DK + b0 + 4 * lg) * 4);
+            buf_store(DKt[t], r, ((16 * t + lr) * 2 * DK + DK + b0 + 4 * lg) * 4);
+        }
+        return;
+    }
     auto write = [&](const f32x4 (&v)[GD_NT], void* out, int64_t ts) {
         const int bytes = (int)ts * (int)sizeof(T);
         const __amdgpu_buffer_rsrc_t r = buf_rsrc((T*)out + t0 * ts + (int64_t)hk * DK, n * bytes);
@@ -627,6 +638,23 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
     };
     write(DQ, a.dq, a.dq_ts);
     write(DKt, a.dk, a.dk_ts);
+}
+
+// dq and dk of the tokens of all sequences, the sums of their heads' in order; four channels to a lane.
+template <typename T>
+__global__ void __launch_bounds__(256) k_gd_sum(GdArgs a) {
+    const int64_t lo = seq_range(a, 0).lo, hi = seq_range(a, a.nseq - 1).hi;
+    const int DK = a.keydim, quads = 2 * DK / 4, groups = a.H / a.share;
+    typedef typename Vec4<T>::type vt;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < (hi - lo) * groups * quads; i += gridDim.x * 256ll) {
+        const int c = (int)(i % quads) * 4, hk = (int)(i / quads % groups);
+        const int64_t t = lo + i / quads / groups;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        for (int m = 0; m < a.share; ++m)
+            v += *(const f32x4*)(a.sums + (((int64_t)hk * a.share + m) * a.tokens + t) * (2 * DK) + c);
+        T* out = c < DK ? (T*)a.dq + t * a.dq_ts + hk * DK + c : (T*)a.dk + t * a.dk_ts + hk * DK + c - DK;
+        *(vt*)out = vt{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+    }
 }
 
 }  // namespace ssd

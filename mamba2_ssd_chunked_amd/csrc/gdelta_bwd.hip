@@ -7,10 +7,16 @@
 
 namespace ssd {
 
-// T and P in three parts, per-token factors, U and Z, entering states and leaving gradients.
+// T and P in three parts, per-token factors, U and Z, entering states and leaving gradients, perhaps dq and dk
+// of every head.
 struct GdBwdWs {
-    size_t T, P, sc, c2, U, Z, S, G, total;
+    size_t T, P, sc, c2, U, Z, S, G, sums, total;
 };
+// Where the chunks of all key heads are too few for the CUs, the heads that share one get a workgroup each, and
+// a launch of its own adds up their dq and dk (23 chunks of 2 key heads of 4 heads: 41 us in turn, 16 and 4 for the sums so).
+static bool heads_apart(const GdArgs& a) {
+    return a.share > 1 && a.tokens / GD_Q * (a.H / a.share) < 256;
+}
 static GdBwdWs bwd_layout(const GdArgs& a, int act) {
     const size_t rows = (size_t)a.H * a.tokens, mat = rows * GD_Q * (act == SSD_BF16 ? 6 : 4);
     const size_t states = (size_t)la_places(a, gd_plan(a)) * a.H * a.keydim * a.valdim * 4;
@@ -23,7 +29,8 @@ static GdBwdWs bwd_layout(const GdArgs& a, int act) {
     w.Z = align256(w.U + rows * a.valdim * 4);
     w.S = align256(w.Z + rows * a.valdim * 4);
     w.G = align256(w.S + states);
-    w.total = align256(w.G + states);
+    w.sums = align256(w.G + states);
+    w.total = heads_apart(a) ? align256(w.sums + rows * a.keydim * 8) : w.sums;
     return w;
 }
 size_t gd_bwd_ws(const GdArgs& a, int act) { return bwd_layout(a, act).total; }
@@ -47,7 +54,11 @@ static hipError_t bwd_dims(const GdArgs& a, hipStream_t s) {
     else if (w.waves == 2) SSD_TRY(walks<T, DK, 1, 2>(a, p, s));
     else if (DV == 64) SSD_TRY(walks<T, DK, 1, 4>(a, p, s));
     else SSD_TRY(walks<T, DK, 2, 4>(a, p, s));
-    return launch(k_gd_chunk<T, DK, DV>, dim3((unsigned)(p.slots * (a.H / a.share))), dim3(DK * 4), s, a, p);
+    const int64_t items = a.sums ? a.H : a.H / a.share;
+    SSD_TRY(launch(k_gd_chunk<T, DK, DV>, dim3((unsigned)(p.slots * items)), dim3(DK * 4), s, a, p));
+    if (!a.sums) return hipSuccess;
+    const int64_t n = (a.tokens * (a.H / a.share) * (DK / 2) + 255) / 256;
+    return launch(k_gd_sum<T>, dim3((unsigned)(n < 1024 ? n : 1024)), dim3(256), s, a);
 }
 
 template <typename T>
@@ -65,6 +76,7 @@ hipError_t launch_gd_bwd(GdArgs a, int act, void* ws, hipStream_t s) {
     a.beta_of = a.out + (size_t)a.H * a.tokens;
     a.U = (float*)(p + w.U), a.Z = (float*)(p + w.Z);
     a.S = (float*)(p + w.S), a.G = (float*)(p + w.G);
+    a.sums = heads_apart(a) ? (float*)(p + w.sums) : nullptr;
     return act == SSD_BF16 ? bwd_t<bf16>(a, s) : bwd_t<float>(a, s);
 }
 

@@ -33,6 +33,7 @@ struct GdArgs {
     double* c2;                               // [H][tokens]: c in units of log 2 (backward)
     float *S, *G;                             // [place][H][DK][DV] states entering, gradients leaving
     float *U, *Z;                             // [H][tokens][DV]
+    float* sums;                              // [H][tokens][2][DK], dq and dk of every head, or null
 };
 size_t gd_fwd_ws(const GdArgs& a, int act);
 size_t gd_bwd_ws(const GdArgs& a, int act);
