@@ -217,44 +217,47 @@ def make_block_norm(*, rows: int, channels: int, act: str | int, res: str | int 
                      int(bool(center)), alpha, eps)
 
 
-def _block_rows(a: _Args, t, name, p: BlockNorm, dtype=None):
-    """(pointer, elements between rows) of [rows, channels] with contiguous channels."""
-    a._base(t, name, dtype or a.act, (p.rows, p.channels))
-    if p.channels > 1 and t.stride(1) != 1:
+def _block_rows(a: _Args, t, name, rows: int, channels: int, dtype):
+    """(pointer, elements between rows; 0 packed) of [rows, channels] with contiguous channels."""
+    a._base(t, name, dtype, (rows, channels))
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    if channels > 1 and t.stride(1) != 1:
         raise ValueError(f"the channels of a row of {name} must be contiguous")
-    step = t.stride(0) if p.rows > 1 else p.channels
-    if step < p.channels:
+    step = t.stride(0) if rows > 1 else channels
+    if step < channels:
         raise ValueError(f"the rows of {name} overlap")
     return t.data_ptr(), step
 
 
 def _block_vectors(a: _Args, p: BlockNorm, z, scale, post_weight, post_bias, pre_weight, pre_bias):
     """Pointers of the channels' vectors; what the problem has no use for is refused."""
-    for want, names in ((p.post, dict(post_weight=post_weight, post_bias=post_bias)),
-                        (p.pre, dict(pre_weight=pre_weight, pre_bias=pre_bias)), (p.gate, dict(z=z))):
-        for name, t in names.items():
-            if not want and t is not None:
-                raise ValueError(f"the problem has no use for {name}")
-    C = (p.channels,)
-    return (a.flat(scale, "scale", C, optional=True),
-            a.flat(post_weight, "post_weight", C, optional=not p.post),
-            a.flat(post_bias, "post_bias", C, optional=True),
-            a.flat(pre_weight, "pre_weight", C, optional=not p.pre),
-            a.flat(pre_bias, "pre_bias", C, optional=True))
+    if not p.post and (post_weight is not None or post_bias is not None):
+        raise ValueError("the problem has no use for post_weight and post_bias")
+    if not p.pre and (pre_weight is not None or pre_bias is not None):
+        raise ValueError("the problem has no use for pre_weight and pre_bias")
+    if not p.gate and z is not None:
+        raise ValueError("the problem has no use for z")
+    C, f = (p.channels,), a.flat
+    return (None if scale is None else f(scale, "scale", C),
+            f(post_weight, "post_weight", C) if p.post else None,
+            None if post_bias is None else f(post_bias, "post_bias", C),
+            f(pre_weight, "pre_weight", C) if p.pre else None,
+            None if pre_bias is None else f(pre_bias, "pre_bias", C))
 
 
 def ssd_block_norm_fwd(problem: BlockNorm, x, y, z, scale, post_weight, post_bias, pre_weight, pre_bias,
                        r, h, stream=None):
-    p = problem
+    p, n, C = problem, problem.rows, problem.channels
     a, c, res = _Args(p.act_dtype), BlockNorm.from_buffer_copy(p), _TORCH_ACT[p.res_dtype]
-    xp, c.x_stride = _block_rows(a, x, "x", p, res)
-    yp, c.y_stride = _block_rows(a, y, "y", p)
+    xp, c.x_stride = _block_rows(a, x, "x", n, C, res)
+    yp, c.y_stride = _block_rows(a, y, "y", n, C, a.act)
     vectors = _block_vectors(a, p, z, scale, post_weight, post_bias, pre_weight, pre_bias)
-    zp, c.z_stride = _block_rows(a, z, "z", p) if p.gate else (None, 0)
-    rp, c.r_stride = _block_rows(a, r, "r", p, res)
+    zp, c.z_stride = _block_rows(a, z, "z", n, C, a.act) if p.gate else (None, 0)
+    rp, c.r_stride = _block_rows(a, r, "r", n, C, res)
     if not p.pre and h is not None:
         raise ValueError("the problem has no use for h")
-    hp, c.h_stride = _block_rows(a, h, "h", p) if p.pre else (None, 0)
+    hp, c.h_stride = _block_rows(a, h, "h", n, C, a.act) if p.pre else (None, 0)
     a.call("ssd_block_norm_fwd", stream, ctypes.byref(c), xp, yp, zp, *vectors, rp, hp)
 
 
@@ -265,21 +268,21 @@ def ssd_block_norm_workspace_bytes(problem: BlockNorm) -> int:
 def ssd_block_norm_bwd(problem: BlockNorm, x, y, z, scale, post_weight, post_bias, pre_weight, dr, dh,
                        dx, dy, dz, dscale, dpost_weight, dpost_bias, dpre_weight, dpre_bias, ws,
                        stream=None):
-    p = problem
+    p, n, C = problem, problem.rows, problem.channels
     a, c, res = _Args(p.act_dtype), BlockNorm.from_buffer_copy(p), _TORCH_ACT[p.res_dtype]
-    xp, c.x_stride = _block_rows(a, x, "x", p, res)
-    yp, c.y_stride = _block_rows(a, y, "y", p)
+    xp, c.x_stride = _block_rows(a, x, "x", n, C, res)
+    yp, c.y_stride = _block_rows(a, y, "y", n, C, a.act)
     vectors = _block_vectors(a, p, z, scale, post_weight, post_bias, pre_weight, None)[:-1]
-    zp, c.z_stride = _block_rows(a, z, "z", p) if p.gate else (None, 0)
+    zp, c.z_stride = _block_rows(a, z, "z", n, C, a.act) if p.gate else (None, 0)
     if dr is None and not p.pre:
         raise ValueError("dr is required")
-    drp, c.r_stride = (None, 0) if dr is None else _block_rows(a, dr, "dr", p, res)
+    drp, c.r_stride = (None, 0) if dr is None else _block_rows(a, dr, "dr", n, C, res)
     if not p.pre and dh is not None:
         raise ValueError("the problem has no use for dh")
-    dhp, c.h_stride = _block_rows(a, dh, "dh", p) if p.pre else (None, 0)
-    dxp, c.dx_stride = _block_rows(a, dx, "dx", p, res)
-    dyp, c.dy_stride = _block_rows(a, dy, "dy", p)
-    dzp, c.dz_stride = _block_rows(a, dz, "dz", p) if p.gate else (None, 0)
+    dhp, c.h_stride = _block_rows(a, dh, "dh", n, C, a.act) if p.pre else (None, 0)
+    dxp, c.dx_stride = _block_rows(a, dx, "dx", n, C, res)
+    dyp, c.dy_stride = _block_rows(a, dy, "dy", n, C, a.act)
+    dzp, c.dz_stride = _block_rows(a, dz, "dz", n, C, a.act) if p.gate else (None, 0)
     sums = [a.flat(t, n, (p.channels,), optional=True)
             for n, t in (("dscale", dscale), ("dpost_weight", dpost_weight), ("dpost_bias", dpost_bias),
                          ("dpre_weight", dpre_weight), ("dpre_bias", dpre_bias))]
@@ -296,15 +299,12 @@ def block_norm_forward(problem: BlockNorm, x, y, z=None, scale=None, post_weight
     and biases [channels] float32, biases and scale optional.  `r` and `h`: tensors to write
     to (r may be x, h may be y or z).
     """
-    p = problem
-    new = []
+    p, made_r, made_h = problem, None, None
     if r is None:
-        r = torch.empty((p.rows, p.channels), dtype=_TORCH_ACT[p.res_dtype], device=x.device)
-        new.append(r)
+        r = made_r = torch.empty((p.rows, p.channels), dtype=_TORCH_ACT[p.res_dtype], device=x.device)
     if h is None and p.pre:
-        h = torch.empty((p.rows, p.channels), dtype=_TORCH_ACT[p.act_dtype], device=x.device)
-        new.append(h)
-    _made_for(stream, x.device, *new)
+        h = made_h = torch.empty((p.rows, p.channels), dtype=_TORCH_ACT[p.act_dtype], device=x.device)
+    _made_for(stream, x.device, made_r, made_h)
     ssd_block_norm_fwd(p, x, y, z, scale, post_weight, post_bias, pre_weight, pre_bias, r, h, stream)
     return r, h
 
