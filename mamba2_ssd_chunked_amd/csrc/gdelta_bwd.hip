@@ -39,7 +39,7 @@ template <typename T, int DK, int CT, int NW>
 static hipError_t walks(const GdArgs& a, const LaPlan& p, hipStream_t s) {
     constexpr int PT = sizeof(T) == 2 ? 3 : 1;
     const dim3 grid = gd_grid(a, a.valdim / (16 * CT * NW)), block(64 * NW);
-    if (NW == 1) SSD_TRY(launch(k_gd_team<T, DK, PT, true>, grid, dim3(256), s, a, p));
+    if constexpr (NW == 1) SSD_TRY(launch(k_gd_team<T, DK, PT, true>, grid, dim3(256), s, a, p));
     else SSD_TRY(launch(k_gd_walk<T, DK, CT, NW, PT, true>, grid, block, s, a, p));
     return launch(k_gd_back<T, DK, CT, NW, PT>, grid, block, s, a, p);
 }
