@@ -31,7 +31,7 @@ extern "C" {
  *
  * Sums, states and decays are float32 (sums of log decays float64) and bf16 outputs are rounded
  * once: a float32 value that meets another operand on its way to a float32 output (states, gate
- * gradients) is taken in parts good to 2^-24, to a bf16 output alone to 2^-16.  A value of q, k, v,
+ * gradients) is taken whole, to a bf16 output alone to 2^-18 of it.  A value of q, k, v,
  * g or beta that is not finite reaches no other sequence and no output before it; the outputs that
  * it reaches (of v: its channel's) and the last state are then not finite.  In the backward
  * it, or one of dout, may reach every gradient of its sequence. */

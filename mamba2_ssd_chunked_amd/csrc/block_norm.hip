@@ -394,7 +394,7 @@ static bool vectors(const BlockArgs& a, int act, int res) {
 template <typename T, typename R, int EL, bool VEC>
 static hipError_t go(const BlockArgs& a, float* part, int threads, hipStream_t s) {
     if (!part) {
-        const int64_t blocks = a.rows < (1 << 22) ? a.rows : (1 << 22);
+        const int64_t blocks = a.rows < (1 << 21) ? a.rows : (1 << 21);
         return launch(k_block_fwd<T, R, EL, VEC>, dim3((unsigned)blocks), dim3(threads), s, a);
     }
     const int n = bwd_blocks(a);

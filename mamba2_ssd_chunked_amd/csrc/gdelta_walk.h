@@ -5,7 +5,7 @@
 // per chunk, where the next chunk's operands have arrived; between, each goes its own way.  With one
 // wave to a SIMD nothing hides an LDS read but the wave's own work: the operands of a product are read
 // while the one before it runs, and the splitting of a result into parts is dealt out between the
-// matrix instructions of the next product (the scheduling groups).
+// matrix instructions of the next product (gd_weave).
 #pragma once
 
 #include "gdelta.h"

@@ -175,3 +175,20 @@ def test_rows_that_are_not_finite_stay_their_own():
     ok = [0, 1, 3, 5]
     assert torch.equal(r[ok], r2[ok]) and torch.equal(h[ok], h2[ok])
     assert torch.isnan(h2[2]).any() and torch.isnan(h2[4]).all()
+
+
+def test_more_rows_than_a_grid_holds_workgroups():
+    """2^22 + 5 rows of workgroups of 1024 threads are more threads than a launch may have; in place.  Every y is
+    one, so that its norm is 1 / sqrt(1 + eps), one in bf16."""
+    import mamba2_ssd_chunked_amd as ssd
+    rows, C = (1 << 22) + 5, 3842
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB of free device memory")
+    x = torch.zeros(rows, C, dtype=torch.bfloat16, device="cuda")
+    y = torch.ones_like(x)
+    p = ssd.make_block_norm(rows=rows, channels=C, act="bf16", pre=False, post=True, gate="none", eps=1e-6)
+    ssd.block_norm_forward(p, x, y, post_weight=torch.ones(C, device="cuda"), r=x)
+    good = all(bool((part == 1).all()) for part in x.split(1 << 18))
+    del x, y
+    torch.cuda.empty_cache()
+    assert good
