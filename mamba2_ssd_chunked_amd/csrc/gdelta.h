@@ -351,19 +351,29 @@ inline dim3 gd_grid(const GdArgs& a, int nblk) {
     return dim3((unsigned)((units + 7) / 8 * 8 * a.share * nblk));
 }
 
-// Waves of a walk's workgroup and column tiles of each.  Every wave reads all of a chunk's operands from LDS, at
-// 64 bytes a cycle for all waves of a CU: few waves to a CU where there are CUs left (a wave of 16 columns is
-// the least; the shard's 256 waves of 2 x 32 x 4 tiles take 467 us on 64 CUs), two tiles to a wave where there
-// are none.
+// Waves of a walk's workgroup and column tiles of each; one wave: a team (gdelta_team.h).  A wave is bound by the
+// instructions that it can issue and its workgroup by the operands that it reads from LDS, so that the fewest waves
+// to a CU are the quickest where there are CUs left, and two tiles to a wave, which share operands, where
+// there are none.  Microseconds of a forward of 2048 tokens (teams, two waves, four, four of two tiles):
+//   bf16, 128 x 128  256 tiles 85 116 - 195, 320 146 120 - 197, 512 166 130 135 207, 768 240 243 160 227,
+//                    1024 321 267 190 250; of 1024 tokens 1536 248 199 161 145, 2048 332 272 190 176
+//   float32          256 152 344 - 585, 512 284 390 385 635, 768 438 758 432 681, 1024 581 798 468 719;
+//                    of 1024 tokens 1536 446 603 434 401
+// Operands of 64 channels move none of the bounds.
 struct GdShape {
     int waves, tiles;
 };
-inline GdShape gd_shape(const GdArgs& a) {
-    const int64_t tiles = (int64_t)a.nseq * a.H * (a.valdim / 16);
-    if (tiles <= 256) return {1, 1};
+inline int64_t gd_tiles(const GdArgs& a) { return (int64_t)a.nseq * a.H * (a.valdim / 16); }
+inline GdShape gd_shape(const GdArgs& a, bool f32) {
+    const int64_t tiles = gd_tiles(a);
+    if (tiles <= (f32 ? 512 : 256)) return {1, 1};
     if (tiles <= 512) return {2, 1};
-    return {4, a.valdim / 64};
+    return {4, tiles <= 1024 ? 1 : a.valdim / 64};
 }
+// The same of the backward's walk, whose waves of two tiles hold too much: two waves or four (128 x 128 in bf16, all
+// of a backward: 256 tiles of single waves 342, 335 of two; 512 tiles 548 and 559, 768 864 and 720; 2048 tiles of 1024
+// tokens 888, of two tiles to a wave 923).
+inline int gd_back_waves(const GdArgs& a) { return gd_tiles(a) <= 512 ? 2 : 4; }
 
 // Spans of one chunk each: numbers of chunks and places of the states that enter them.
 inline LaPlan gd_plan(const GdArgs& a) {

@@ -6,25 +6,25 @@
 
 namespace ssd {
 
-template <typename T, int BD, int CT, int NW, int PT>
+template <typename T, int BD, int NW, int PT>
 struct GdBackLds {
     static constexpr int k = 0, q = k + GdTile<T, BD>::BYTES, d = q + GdTile<T, BD>::BYTES,
-                         t = d + GdTile<T, 16 * CT * NW>::BYTES, p = t + GdMat<T, PT>::BYTES,
+                         t = d + GdTile<T, 16 * NW>::BYTES, p = t + GdMat<T, PT>::BYTES,
                          sc = p + GdMat<T, PT>::BYTES, bytes = (sc + (int)sizeof(GdScalars) + 1023) / 1024 * 1024;
     static constexpr int buffers = 2 * bytes <= 160 * 1024 ? 2 : 1;
 };
 
 // The gradient G of the state, as the forward walk keeps S: a wave owns columns of G^T.
-template <typename T, int BD, int CT, int NW, int PT>
+template <typename T, int BD, int NW, int PT>
 __global__ void __launch_bounds__(64 * NW) k_gd_back(GdArgs a, LaPlan plan) {
     typedef Mma<T> M;
     typedef typename M::Frag Frag;
-    typedef GdBackLds<T, BD, CT, NW, PT> L;
+    typedef GdBackLds<T, BD, NW, PT> L;
     typedef GdTile<T, BD> Tile;
-    typedef GdTile<T, 16 * CT * NW> TileV;
+    typedef GdTile<T, 16 * NW> TileV;
     typedef GdMat<T, PT> Mat;
     constexpr int KS = M::KS, KB = BD / KS, TPK = LaCfg<T>::TPK, NK = GD_Q / KS;
-    constexpr int BT = BD / 16, CDW = 16 * CT * NW;
+    constexpr int BT = BD / 16, CDW = 16 * NW;
     __shared__ __align__(1024) char lds[L::buffers * L::bytes];
 
     const int nblk = a.valdim / CDW;
@@ -80,15 +80,13 @@ __global__ void __launch_bounds__(64 * NW) k_gd_back(GdArgs a, LaPlan plan) {
     };
     if (L::buffers == 2 && nch > 0) stage_all(nch - 1);
 
-    f32x4 G[BT][CT];
-    const int cw = wave * 16 * CT, col = c0 + cw + lr;
+    f32x4 G[BT];
+    const int cw = wave * 16, col = c0 + cw + lr;
     const int64_t state_at = ((int64_t)it.s * a.H + h) * ((int64_t)BD * DV);
-    auto at = [&](int t, int u) { return (col + 16 * u) * BD + la_channel<T>(t, lg); };
+    auto at = [&](int t) { return col * BD + la_channel<T>(t, lg); };
 #pragma unroll
     for (int t = 0; t < BT; ++t)
-#pragma unroll
-        for (int u = 0; u < CT; ++u)
-            G[t][u] = a.dfin ? *(const f32x4*)(a.dfin + state_at + at(t, u)) : f32x4{0.f, 0.f, 0.f, 0.f};
+        G[t] = a.dfin ? *(const f32x4*)(a.dfin + state_at + at(t)) : f32x4{0.f, 0.f, 0.f, 0.f};
 
     for (int k = nch - 1; k >= 0; --k) {
         const int n = tokens_of(k);
@@ -98,7 +96,7 @@ __global__ void __launch_bounds__(64 * NW) k_gd_back(GdArgs a, LaPlan plan) {
             stage_all(k);
         }
         // behind this chunk's fetches stand only the last chunk's stores of Z
-        if (L::buffers == 2 && k + 1 < nch) gd_wait<16 * CT>();
+        if (L::buffers == 2 && k + 1 < nch) gd_wait<16>();
         else gd_wait<0>();
         __syncthreads();
         if (k + 1 < nch) {  // the gradient behind chunk k is kept where the state that enters k + 1 is
@@ -106,9 +104,7 @@ __global__ void __launch_bounds__(64 * NW) k_gd_back(GdArgs a, LaPlan plan) {
 #pragma unroll
             for (int t = 0; t < BT; ++t)
 #pragma unroll
-                for (int u = 0; u < CT; ++u)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) g[(la_channel<T>(t, lg) + r) * DV + col + 16 * u] = G[t][u][r];
+                for (int r = 0; r < 4; ++r) g[(la_channel<T>(t, lg) + r) * DV + col] = G[t][r];
         }
         const Next nx = next_of(k > 0 ? k - 1 : 0, k + 1);
         constexpr int PLACES = KB + 2 * NK;
@@ -121,16 +117,12 @@ __global__ void __launch_bounds__(64 * NW) k_gd_back(GdArgs a, LaPlan plan) {
         const GdScalars* sc = (const GdScalars*)(buf + L::sc);
 
         // P^T do + e^(C - c) K G^T
-        f32x4 x[GD_NT][CT], y[GD_NT][CT];
+        f32x4 x[GD_NT], y[GD_NT];
 #pragma unroll
-        for (int t = 0; t < GD_NT; ++t)
+        for (int t = 0; t < GD_NT; ++t) x[t] = y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        Frag df[NK];
 #pragma unroll
-            for (int u = 0; u < CT; ++u) x[t][u] = y[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-        Frag df[NK][CT];
-#pragma unroll
-        for (int b = 0; b < NK; ++b)
-#pragma unroll
-            for (int u = 0; u < CT; ++u) df[b][u] = TileV::xt(sd, KS * b, cw + 16 * u, lane);
+        for (int b = 0; b < NK; ++b) df[b] = TileV::xt(sd, KS * b, cw, lane);
         Frag f[KB][GD_NT];
 #pragma unroll
         for (int q = 0; q < KB; ++q)
@@ -139,20 +131,15 @@ __global__ void __launch_bounds__(64 * NW) k_gd_back(GdArgs a, LaPlan plan) {
         if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
         gd_for<KB>([&](auto Q) {
             constexpr int q = decltype(Q)::value;
-            Frag gf[CT][PT];
+            Frag gf[PT];
+            f32x4 tl[TPK];
 #pragma unroll
-            for (int u = 0; u < CT; ++u) {
-                f32x4 tl[TPK];
-#pragma unroll
-                for (int e = 0; e < TPK; ++e) tl[e] = G[q * TPK + e][u];
-                gd_split<T, PT>(tl, gf[u]);
-            }
+            for (int e = 0; e < TPK; ++e) tl[e] = G[q * TPK + e];
+            gd_split<T, PT>(tl, gf);
 #pragma unroll
             for (int p = PT - 1; p >= 0; --p)
 #pragma unroll
-                for (int t = 0; t < GD_NT; ++t)
-#pragma unroll
-                    for (int u = 0; u < CT; ++u) y[t][u] = M::mma(f[q][t], gf[u][p], y[t][u]);
+                for (int t = 0; t < GD_NT; ++t) y[t] = M::mma(f[q][t], gf[p], y[t]);
             ahead(Q);
         });
         gd_for<NK>([&](auto B) {
@@ -166,33 +153,25 @@ __global__ void __launch_bounds__(64 * NW) k_gd_back(GdArgs a, LaPlan plan) {
 #pragma unroll
             for (int p = PT - 1; p >= 0; --p)
 #pragma unroll
-                for (int t = 0; t < (b + 1) * TPK; ++t)
-#pragma unroll
-                    for (int u = 0; u < CT; ++u) x[t][u] = M::mma(pf[t][p], df[b][u], x[t][u]);
+                for (int t = 0; t < (b + 1) * TPK; ++t) x[t] = M::mma(pf[t][p], df[b], x[t]);
         });
 #pragma unroll
         for (int t = 0; t < GD_NT; ++t) {
             const f32x4 w = *(const f32x4*)(sc->out + 16 * t + 4 * lg);
-#pragma unroll
-            for (int u = 0; u < CT; ++u) x[t][u] += w * y[t][u];
+            x[t] += w * y[t];
         }
 
         // Z = T^T of that
-        f32x4 z[GD_NT][CT];
+        f32x4 z[GD_NT];
 #pragma unroll
-        for (int t = 0; t < GD_NT; ++t)
-#pragma unroll
-            for (int u = 0; u < CT; ++u) z[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < GD_NT; ++t) z[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         gd_for<NK>([&](auto B) {
             constexpr int b = NK - 1 - decltype(B)::value;
-            Frag xf[CT][PT];
+            Frag xf[PT];
+            f32x4 tl[TPK];
 #pragma unroll
-            for (int u = 0; u < CT; ++u) {
-                f32x4 tl[TPK];
-#pragma unroll
-                for (int e = 0; e < TPK; ++e) tl[e] = x[b * TPK + e][u];
-                gd_split<T, PT>(tl, xf[u]);
-            }
+            for (int e = 0; e < TPK; ++e) tl[e] = x[b * TPK + e];
+            gd_split<T, PT>(tl, xf);
             Frag tf[GD_NT][PT];
 #pragma unroll
             for (int t = 0; t < (b + 1) * TPK; ++t)
@@ -204,71 +183,56 @@ __global__ void __launch_bounds__(64 * NW) k_gd_back(GdArgs a, LaPlan plan) {
 #pragma unroll
                 for (int p = 0; p <= s; ++p)
 #pragma unroll
-                    for (int t = 0; t < (b + 1) * TPK; ++t)
-#pragma unroll
-                        for (int u = 0; u < CT; ++u) z[t][u] = M::mma(tf[t][p], xf[u][s - p], z[t][u]);
+                    for (int t = 0; t < (b + 1) * TPK; ++t) z[t] = M::mma(tf[t][p], xf[s - p], z[t]);
         });
         const __amdgpu_buffer_rsrc_t r = buf_rsrc(a.Z + (hrow + t0) * DV, n * DV * 4);
 #pragma unroll
         for (int t = 0; t < GD_NT; ++t)
 #pragma unroll
-            for (int u = 0; u < CT; ++u)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    __builtin_amdgcn_raw_buffer_store_b32(
-                        __float_as_uint(z[t][u][q]), r, ((16 * t + 4 * lg + q) * DV + col + 16 * u) * 4, 0, 0);
+            for (int q = 0; q < 4; ++q)
+                __builtin_amdgcn_raw_buffer_store_b32(
+                    __float_as_uint(z[t][q]), r, ((16 * t + 4 * lg + q) * DV + col) * 4, 0, 0);
 
         // G <- e^C G + scale (e^c do)^T Q - (e^c B Z)^T K
         const float keep = sc->in[n - 1];
 #pragma unroll
-        for (int t = 0; t < BT; ++t)
-#pragma unroll
-            for (int u = 0; u < CT; ++u) G[t][u] *= keep;
+        for (int t = 0; t < BT; ++t) G[t] *= keep;
         gd_for<NK>([&](auto B) {
             constexpr int b = decltype(B)::value;
-            Frag wf[CT][PT], zf[CT][PT];
+            Frag wf[PT], zf[PT];
+            f32x4 tl[TPK], tz[TPK];
 #pragma unroll
-            for (int u = 0; u < CT; ++u) {
-                f32x4 tl[TPK], tz[TPK];
+            for (int e = 0; e < TPK; ++e) {
+                const int t = b * TPK + e;
+                const f32x4 in = *(const f32x4*)(sc->in + 16 * t + 4 * lg);
+                const f32x4 be = *(const f32x4*)(sc->beta + 16 * t + 4 * lg);
 #pragma unroll
-                for (int e = 0; e < TPK; ++e) {
-                    const int t = b * TPK + e;
-                    const f32x4 in = *(const f32x4*)(sc->in + 16 * t + 4 * lg);
-                    const f32x4 be = *(const f32x4*)(sc->beta + 16 * t + 4 * lg);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        tl[e][i] = a.scale * in[i] * (float)df[b][u][4 * e + i];
-                        tz[e][i] = -in[i] * be[i] * z[t][u][i];
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    tl[e][i] = a.scale * in[i] * (float)df[b][4 * e + i];
+                    tz[e][i] = -in[i] * be[i] * z[t][i];
                 }
-                gd_split<T, PT>(tl, wf[u]);
-                gd_split<T, PT>(tz, zf[u]);
             }
+            gd_split<T, PT>(tl, wf);
+            gd_split<T, PT>(tz, zf);
             Frag fb[BT];
 #pragma unroll
             for (int t = 0; t < BT; ++t) fb[t] = Tile::bt(sq, KS * b, t, lane);
 #pragma unroll
             for (int p = PT - 1; p >= 0; --p)
 #pragma unroll
-                for (int t = 0; t < BT; ++t)
-#pragma unroll
-                    for (int u = 0; u < CT; ++u) G[t][u] = M::mma(fb[t], wf[u][p], G[t][u]);
+                for (int t = 0; t < BT; ++t) G[t] = M::mma(fb[t], wf[p], G[t]);
 #pragma unroll
             for (int t = 0; t < BT; ++t) fb[t] = Tile::bt(sk, KS * b, t, lane);
 #pragma unroll
             for (int p = PT - 1; p >= 0; --p)
 #pragma unroll
-                for (int t = 0; t < BT; ++t)
-#pragma unroll
-                    for (int u = 0; u < CT; ++u) G[t][u] = M::mma(fb[t], zf[u][p], G[t][u]);
+                for (int t = 0; t < BT; ++t) G[t] = M::mma(fb[t], zf[p], G[t]);
         });
     }
     gd_wait<0>();  // a workgroup's LDS is another's once its waves have ended
     if (a.dinit) {
 #pragma unroll
-        for (int t = 0; t < BT; ++t)
-#pragma unroll
-            for (int u = 0; u < CT; ++u) *(f32x4*)(a.dinit + state_at + at(t, u)) = G[t][u];
+        for (int t = 0; t < BT; ++t) *(f32x4*)(a.dinit + state_at + at(t)) = G[t];
     }
 }
 

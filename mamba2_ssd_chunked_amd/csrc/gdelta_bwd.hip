@@ -13,7 +13,8 @@ struct GdBwdWs {
     size_t T, P, sc, c2, U, Z, S, G, sums, total;
 };
 // Where the chunks of all key heads are too few for the CUs, the heads that share one get a workgroup each, and
-// a launch of its own adds up their dq and dk (23 chunks of 2 key heads of 4 heads: 41 us in turn, 16 and 4 for the sums so).
+// a launch of its own adds up their dq and dk (16 chunks of 2 key heads of 4 heads, 64 x 64: 41 us in turn, 16 and 4
+// for the sums so).
 static bool heads_apart(const GdArgs& a) {
     return a.share > 1 && a.tokens / GD_Q * (a.H / a.share) < 256;
 }
@@ -35,25 +36,34 @@ static GdBwdWs bwd_layout(const GdArgs& a, int act) {
 }
 size_t gd_bwd_ws(const GdArgs& a, int act) { return bwd_layout(a, act).total; }
 
-template <typename T, int DK, int CT, int NW>
-static hipError_t walks(const GdArgs& a, const LaPlan& p, hipStream_t s) {
+template <typename T, int DK>
+static hipError_t walk(const GdArgs& a, const LaPlan& p, hipStream_t s) {
     constexpr int PT = sizeof(T) == 2 ? 3 : 1;
-    const dim3 grid = gd_grid(a, a.valdim / (16 * CT * NW)), block(64 * NW);
-    if constexpr (NW == 1) SSD_TRY(launch(k_gd_team<T, DK, PT, true>, grid, dim3(256), s, a, p));
-    else SSD_TRY(launch(k_gd_walk<T, DK, CT, NW, PT, true>, grid, block, s, a, p));
-    return launch(k_gd_back<T, DK, CT, NW, PT>, grid, block, s, a, p);
+    const GdShape w = gd_shape(a, sizeof(T) == 4);
+    const dim3 grid = gd_grid(a, a.valdim / (16 * w.tiles * w.waves));
+    if (w.waves == 1) return launch(k_gd_team<T, DK, PT, true>, grid, dim3(256), s, a, p);
+    if constexpr (sizeof(T) == 2)
+        if (w.waves == 2) return launch(k_gd_walk<T, DK, 1, 2, PT, true>, grid, dim3(128), s, a, p);
+    if (w.tiles == 1) return launch(k_gd_walk<T, DK, 1, 4, PT, true>, grid, dim3(256), s, a, p);
+    return launch(k_gd_walk<T, DK, 2, 4, PT, true>, grid, dim3(256), s, a, p);
+}
+
+template <typename T, int DK>
+static hipError_t walk_back(const GdArgs& a, const LaPlan& p, hipStream_t s) {
+    constexpr int PT = sizeof(T) == 2 ? 3 : 1;
+    const int waves = gd_back_waves(a);
+    const dim3 grid = gd_grid(a, a.valdim / (16 * waves));
+    if (waves == 2) return launch(k_gd_back<T, DK, 2, PT>, grid, dim3(128), s, a, p);
+    return launch(k_gd_back<T, DK, 4, PT>, grid, dim3(256), s, a, p);
 }
 
 template <typename T, int DK, int DV>
 static hipError_t bwd_dims(const GdArgs& a, hipStream_t s) {
     constexpr int PT = sizeof(T) == 2 ? 3 : 1;
     const LaPlan p = gd_plan(a);
-    const GdShape w = gd_shape(a);
     SSD_TRY(launch(k_gd_prep<T, DK, PT, PT, false>, dim3((unsigned)(p.slots * a.H)), dim3(256), s, a, p));
-    if (w.waves == 1) SSD_TRY(walks<T, DK, 1, 1>(a, p, s));
-    else if (w.waves == 2) SSD_TRY(walks<T, DK, 1, 2>(a, p, s));
-    else if (DV == 64) SSD_TRY(walks<T, DK, 1, 4>(a, p, s));
-    else SSD_TRY(walks<T, DK, 2, 4>(a, p, s));
+    SSD_TRY((walk<T, DK>(a, p, s)));
+    SSD_TRY((walk_back<T, DK>(a, p, s)));
     const int64_t items = a.sums ? a.H : a.H / a.share;
     SSD_TRY(launch(k_gd_chunk<T, DK, DV>, dim3((unsigned)(p.slots * items)), dim3(DK * 4), s, a, p));
     if (!a.sums) return hipSuccess;

@@ -24,11 +24,12 @@ template <typename T, int DK, int PT>
 static hipError_t fwd_parts(const GdArgs& a, hipStream_t s) {
     constexpr int PO = sizeof(T) == 2 ? 2 : 1;
     const LaPlan p = gd_plan(a);
-    const GdShape w = gd_shape(a);
+    const GdShape w = gd_shape(a, sizeof(T) == 4);
     SSD_TRY(launch(k_gd_prep<T, DK, PT, PO, true>, dim3((unsigned)(p.slots * a.H)), dim3(256), s, a, p));
     const dim3 grid = gd_grid(a, a.valdim / (16 * w.waves * w.tiles));
     if (w.waves == 1) return launch(k_gd_team<T, DK, PT, false>, grid, dim3(256), s, a, p);
-    if (w.waves == 2) return launch(k_gd_walk<T, DK, 1, 2, PT, false>, grid, dim3(128), s, a, p);
+    if constexpr (sizeof(T) == 2)
+        if (w.waves == 2) return launch(k_gd_walk<T, DK, 1, 2, PT, false>, grid, dim3(128), s, a, p);
     if (w.tiles == 1) return launch(k_gd_walk<T, DK, 1, 4, PT, false>, grid, dim3(256), s, a, p);
     return launch(k_gd_walk<T, DK, 2, 4, PT, false>, grid, dim3(256), s, a, p);
 }

@@ -9,7 +9,7 @@ from test_gpu_gdelta import check_backward, check_forward, make, problem
 pytestmark = pytest.mark.gpu
 
 FEW = [70, 0, 1, 64, 129, 5, 40, 33, 66]  # 9 sequences; of 8 heads 288 tiles of 16 channels of 64, 576 of 128
-MANY = FEW + [7, 65, 2, 100, 63, 31, 128, 3]  # 17 sequences: 544 tiles of 64
+MANY = FEW + [7, 65, 2, 100, 63, 31, 128, 3]  # 17 sequences: 544 tiles of 64, 1088 of 128
 CASES = [
     dict(lens=FEW, H=8, Hk=4, Dk=128, Dv=64, before=3, behind=6),
     dict(lens=FEW, H=8, Hk=2, Dk=64, Dv=64, gates="edges"),
@@ -18,6 +18,8 @@ CASES = [
     dict(lens=MANY, H=8, Hk=1, Dk=128, Dv=64, behind=80),
     dict(lens=FEW, H=8, Hk=4, Dk=128, Dv=128, gates="edges"),
     dict(lens=FEW, H=9, Hk=3, Dk=64, Dv=128, init=False),
+    dict(lens=MANY, H=8, Hk=2, Dk=128, Dv=128, fused=True),
+    dict(lens=MANY, H=8, Hk=4, Dk=64, Dv=128, gates="edges"),
     dict(lens=FEW[:5], H=16, Hk=8, Dk=128, Dv=64, before=900, behind=900),  # 32 chunks of 8 key heads or more:
     dict(lens=FEW[:5], H=16, Hk=8, Dk=64, Dv=128, before=70, behind=1720),  # their heads in turn
 ]
@@ -42,7 +44,7 @@ def test_backward(case, act):
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
-@pytest.mark.parametrize("case", [CASES[0], CASES[3], CASES[5]], ids=name)
+@pytest.mark.parametrize("case", [CASES[0], CASES[3], CASES[5], CASES[7]], ids=name)
 def test_values_that_are_not_finite(case, act):
     """One in the middle of a sequence of more than a chunk reaches no other sequence and, forward, no earlier
     token."""
