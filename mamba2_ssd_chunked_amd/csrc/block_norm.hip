@@ -9,7 +9,9 @@
 // Bound by HBM: every tensor is read or written once.  A workgroup holds a row in registers, EL
 // channels to a thread, between its statistics and its outputs; in the backward it goes over
 // several rows and keeps the five sums of its channels in registers, which a second launch adds up
-// in a fixed order.
+// in a fixed order.  16384 rows of 2048 bf16 channels with a float32 residual: forward 100 us, 4.7 TB/s; backward
+// 203 us, 3.6 TB/s of its 740 MB, its rows' three rounds of sums in a row not all hidden, and the second launch
+// 13 us.  Its sums are what a thread's registers allow: four channels a thread (below).
 #include "layer_internal.h"
 
 namespace ssd {

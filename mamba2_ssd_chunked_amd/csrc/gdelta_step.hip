@@ -2,7 +2,8 @@
 //   S <- a S,  u = beta (v - S k),  S <- S + u k^T,  o = scale S q     (S of [valdim][keydim])
 // A lane owns four neighbouring key channels of some rows of S, a group of keydim / 4 lanes a whole row;
 // the state passes through registers once per call, however many tokens it has.  Bound by HBM, 8
-// bytes per state element.
+// bytes per state element: 256 rows of 32 heads of 128 x 128 take 211 us, 5.1 TB/s; one row 6.2 us, a launch and the
+// trip to memory and back.
 #include <cfloat>
 
 #include "layer_internal.h"

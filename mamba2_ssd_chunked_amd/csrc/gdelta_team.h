@@ -2,10 +2,10 @@
 // channels, where a wave each would leave most of the chip idle.
 //
 // One wave issues some thousand instructions per chunk and 16 channels, so that the shard's 256 column tiles
-// (2 rows, 32 heads of 64 channels) keep 256 of 1024 SIMDs busy for 460 us.  Here wave w owns a quarter
+// (2 rows, 32 heads of 64 channels) keep 256 of 1024 SIMDs busy for 460 us; teams take 300.  Here wave w owns a quarter
 // of the state's key channels and token tile w of X, R, U and O, and what one has and all need
 // goes through LDS in parts, as operands:
-//   parts of S  |  X_w = K_w S^T, R_w  |  parts of R  |  U_w = T_w R  |  parts of U  |  O_w, its channels of S
+//   parts of S  |  X_w = K_w S^T, parts of R_w  |  U_w = T_w R, its parts  |  O_w, its channels of S
 // with a barrier at each bar.  An operand is fetched into LDS as soon as its place is free: a chunk
 // ahead of its use at most.
 #pragma once
