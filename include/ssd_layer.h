@@ -80,7 +80,7 @@ int ssd_gdelta_fwd(const ssd_gdelta* problem, int32_t nseq, const void* q, const
  *   dk_t = D^T u_t - a_t S_(t-1)^T (beta_t du)       (dq, dk: summed over the heads that share them)
  *   dbeta_t = du . (v_t - a_t S_(t-1) k_t),  dg_t = <B, a_t S_(t-1)>
  *   G_(t-1) = a_t B,  dinit = G before the first token (dfinal where a sequence is empty)
- * The states are recomputed.
+ * The states are recomputed.  No output may share memory with an input.
  *   dout       [batch][seqlen][H][valdim]                                      (in)
  *   dfinal     [nseq][H][valdim][keydim] float32 or NULL                       (in)
  *   dq, dk, dv as q, k, v; dg, dbeta [batch][seqlen][H] float32; tokens outside
