@@ -185,13 +185,16 @@ __device__ __forceinline__ gd_i4 gd_rsrc(const void* p, int bytes) {
 __device__ __forceinline__ unsigned gd_lds(const void* p) {
     return __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
 }
+// The compiler does not look into the assembly: a descriptor that a vector instruction wrote (v_readfirstlane, or
+// v_readlane of a spilled one) may be read by a vector memory instruction five wait states later only, so that each
+// load brings its own five, the move to m0 and s_nop 3.
 __device__ __forceinline__ void gd_dma16(gd_i4 r, unsigned lds, int off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
-                 : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void gd_dma4(gd_i4 r, unsigned lds, int off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
-                 : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
+                 : "memory", "m0");
 }
 // Until at most N of this wave's memory accesses are on their way: all but the last N are done.
 template <int N>
