@@ -27,7 +27,7 @@ extern "C" {
  * are taken as they are; a model makes them unit length before (ssd_norm_fwd with a group per
  * head and weights of keydim^-1/2 does).  g_t <= 0 is meant (minus infinity: nothing before t
  * is kept); larger values are not refused as long as the exponentials of their sums over 64 tokens
- * stay within float32's range.  beta_t may be any value.
+ * (of single tokens that of g_t / 2) stay within float32's range.  beta_t may be any value.
  *
  * Sums, states and decays are float32 (sums of log decays float64) and bf16 outputs are rounded
  * once: a float32 value that meets another operand on its way to a float32 output (states, gate

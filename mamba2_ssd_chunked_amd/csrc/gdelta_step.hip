@@ -48,8 +48,15 @@ __global__ void __launch_bounds__(256) k_gd_step(GdStep a) {
         const f32x4 q = gd_load4((const T*)a.q + tok * a.q_ts + h / a.share * BD + col);
         const f32x4 k = gd_load4((const T*)a.k + tok * a.k_ts + h / a.share * BD + col);
         const T* v = (const T*)a.v + tok * a.v_ts + (int64_t)h * a.valdim + d0;
-        float keep = expf(a.g[tok * a.g_ts + h]);
-        if (keep == INFINITY) keep = FLT_MAX;  // a state of zeros stays one
+        const float g = a.g[tok * a.g_ts + h];
+        float keep = expf(g);
+        if (keep == INFINITY) {
+            // Beyond float32: by the root, here and below, so that a state of zeros stays one and a product that
+            // float32 holds is right.  A g of infinity is not finite and leaves nothing that is, as in a prompt.
+            keep = g < INFINITY ? fminf(expf(0.5f * g), FLT_MAX) : NAN;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) m[i] *= keep;
+        }
         const float beta = a.beta[tok * a.b_ts + h];
         float mine = 0.f;
 #pragma unroll
