@@ -81,6 +81,9 @@ int ssd_gdelta_fwd(const ssd_gdelta* problem, int32_t nseq, const void* q, const
  *   dbeta_t = du . (v_t - a_t S_(t-1) k_t),  dg_t = <B, a_t S_(t-1)>
  *   G_(t-1) = a_t B,  dinit = G before the first token (dfinal where a sequence is empty)
  * The states are recomputed.  No output may share memory with an input.
+ * dg_t is formed as a sum, over the tokens i from t to the end of a run of 64, of q_i . dq_i - v_i . dv_i, and of
+ * <G, S> behind the run: it is good to some 2^-20 of these terms, which a strong decay at t does not make
+ * smaller as it does dg_t (of e^g below 1e-6 little of dg_t is left).  Where e^(g_t) is zero in float32 dg_t is zero.
  *   dout       [batch][seqlen][H][valdim]                                      (in)
  *   dfinal     [nseq][H][valdim][keydim] float32 or NULL                       (in)
  *   dq, dk, dv as q, k, v; dg, dbeta [batch][seqlen][H] float32; tokens outside

@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
             DKt[t] += gu[t];
         }
         __syncthreads();
-        if (wave == 0) {  // dg_t: the sum from t on
+        if (wave == 0) {  // dg_t: the sum from t on; zero, not the sum's roundings, where nothing before t is kept
             double d = -(double)zv[lane], all = 0.0;
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
@@ -574,7 +574,8 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
                 const double down = __shfl_down(d, o, 64);
                 if (lane + o < 64) d += down;
             }
-            if (lane < n) a.dg[(t0 + lane) * a.H + h] = (float)(d + all);
+            const float keep = __builtin_amdgcn_exp2f((float)(c2[lane] - (lane > 0 ? c2[lane - 1] : 0.0)));
+            if (lane < n) a.dg[(t0 + lane) * a.H + h] = keep == 0.f ? 0.f : (float)(d + all);
         }
     }
 
