@@ -47,6 +47,10 @@ namespace ssd {
 
 constexpr int GD_Q = GD_CHUNK, GD_NT = GD_Q / 16;
 
+// The smallest beta that the backward's walks count with, since dbeta is divided by it; what it adds to states is
+// far below float32's precision of what they stand for.  The chunks' gradients take the given one.
+constexpr float GD_BETA_MIN = 9.094947017729282e-13f;  // 2^-40
+
 // Parts of a float32 value as an operand: bf16 rounded, and so the remainders, which are exact.  Two
 // leave out 2^-18 of it, three nothing.  The remainder of a value of a pair is one dot product, of the pair's
 // bf16 and (-1, 0) or (0, -1), where taking the part apart and subtracting it would be two

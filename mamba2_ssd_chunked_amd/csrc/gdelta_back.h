@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
         const T* pd = (const T*)a.dout + t0 * a.o_ts + (int64_t)h * DV;
         const bool live = threadIdx.x < n;
         const float rin = live ? a.in[row0 + threadIdx.x] : 0.f, rout = live ? a.out[row0 + threadIdx.x] : 0.f;
-        const float rbeta = live ? a.beta_of[row0 + threadIdx.x] : 1.f;
+        const float rbeta = live ? a.beta[(t0 + threadIdx.x) * a.b_ts + h] : 1.f;
         const double rc = live ? a.c2[row0 + threadIdx.x] : -1e30;  // no factor of a row without a token
         GdRows<T, DV, NTHR> rd;
         if constexpr (L::DO) rd.load((const T*)a.dout + (int64_t)h * DV, a.o_ts, t0, n);
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
             const int y = i * NTHR + threadIdx.x, row = y / VPR, c = y % VPR * 8;
-            be[i] = row < n ? a.beta_of[row0 + row] : 1.f;
+            be[i] = row < n ? a.beta[(t0 + row) * a.b_ts + h] : 1.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 u[i][e] = buf_load<f32x4>(ru, (row * DV + c + 4 * e) * 4);
@@ -383,8 +383,11 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
             }
             if (y % VPR == 0) {
                 zv[row] = vz;
-                if (row < n) a.dbeta[(t0 + row) * a.H + h] = zu / be[i];
+                if (row < n) a.dbeta[(t0 + row) * a.H + h] = zu / (fabsf(be[i]) < GD_BETA_MIN ? copysignf(GD_BETA_MIN, be[i]) : be[i]);
             }
+            // U of a beta smaller than the walk's, so that all of dk that is this token's has the given one as a factor
+            const float share = fabsf(be[i]) < GD_BETA_MIN ? fabsf(be[i]) * (1.f / GD_BETA_MIN) : 1.f;
+            u[i][0] *= share, u[i][1] *= share;
             if constexpr (sizeof(T) == 2) {
                 Frag f[P::U], g[P::Z];
                 gd_split<T, P::U>(u[i], f);

@@ -11,10 +11,6 @@
 
 namespace ssd {
 
-// The smallest beta of the backward, which divides by it; the change is far below float32's
-// precision of anything that beta meets.
-constexpr float GD_BETA_MIN = 9.094947017729282e-13f;  // 2^-40
-
 // PT, PP: parts of T and P.  TAME: a key, g or beta that is not finite ends the chunk at its row (k and
 // beta count as zero from there on, and `out` tells the rows); else it spreads over the chunk.
 template <typename T, int DK, int PT, int PP, bool TAME>
