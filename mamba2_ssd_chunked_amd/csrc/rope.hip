@@ -11,7 +11,8 @@ namespace ssd {
 // V: neighbouring channels that a thread moves at once, 8, or 1 where sizes or alignment ask for it.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) k_rope(RopeArgs a) {
-    typedef T vt __attribute__((ext_vector_type(V)));
+    // rows are known to be aligned to 16 bytes, or to their elements, and no further
+    typedef T vt __attribute__((ext_vector_type(V), aligned(V == 1 ? sizeof(T) : 16)));
     __shared__ float cs[ROPE_MAX_DIM / 2], sn[ROPE_MAX_DIM / 2];
     const int half = a.R / 2;
     const bool pairs = a.style == SSD_ROPE_HALF;
