@@ -27,11 +27,13 @@ extern "C" {
  * are taken as they are; a model makes them unit length before (ssd_norm_fwd with a group per
  * head and weights of keydim^-1/2 does).  g_t <= 0 is meant (minus infinity: nothing before t
  * is kept); larger values are not refused as long as the exponentials of their sums over 64 tokens
- * (of single tokens that of g_t / 2) stay within float32's range.  beta_t may be any value.
+ * (of single tokens that of g_t / 2) stay within float32's range.  beta_t may be any value with which
+ * u_t does.
  *
  * Sums, states and decays are float32 (sums of log decays float64) and bf16 outputs are rounded
  * once: a float32 value that meets another operand on its way to a float32 output (states, gate
- * gradients) is taken whole, to a bf16 output alone to 2^-18 of it.  A value of q, k, v,
+ * gradients) is taken whole, to a bf16 output alone to 2^-18 of it.  (The states are on their way to a float32
+ * output if a last state is asked for, so that the last bits of bf16 outputs may depend on that.)  A value of q, k, v,
  * g or beta that is not finite reaches no other sequence and no output before it; the outputs that
  * it reaches (of v: its channel's) and the last state are then not finite.  In the backward
  * it, or one of dout, may reach every gradient of its sequence. */

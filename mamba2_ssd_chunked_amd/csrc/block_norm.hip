@@ -10,8 +10,10 @@
 // channels to a thread, between its statistics and its outputs; in the backward it goes over
 // several rows and keeps the five sums of its channels in registers, which a second launch adds up
 // in a fixed order.  16384 rows of 2048 bf16 channels with a float32 residual: forward 100 us, 4.7 TB/s; backward
-// 203 us, 3.6 TB/s of its 740 MB, its rows' three rounds of sums in a row not all hidden, and the second launch
-// 13 us.  Its sums are what a thread's registers allow: four channels a thread (below).
+// 203 us, 3.6 TB/s of its 740 MB, since a row's loads do not overlap the sums of the one before (below), and the
+// second launch 13 us.  Its sums are what a thread's registers allow, 128 with 1024 threads: four channels a thread.
+// Rows of more than 4096 channels have 8 or 16 and spill in the backward, without vectors in the forward too: 16384 x
+// 5120 235 and 1138 us (one channel at a time 841 and 3073), 8192 x 10240 319 and 3916 (1764 and 21788).
 #include "layer_internal.h"
 
 namespace ssd {
@@ -238,7 +240,9 @@ __global__ void __launch_bounds__(1024) k_block_bwd(BlockArgs a, float* __restri
     float ds[EL], dw1[EL], db1[EL], dw2[EL], db2[EL];
 #pragma unroll
     for (int e = 0; e < EL; ++e) ds[e] = dw1[e] = db1[e] = dw2[e] = db2[e] = 0.f;
-    // Where registers allow, the next row is on its way while one is computed.
+    // Where registers allow, the next row is asked for before one is computed.  The loads' conditions (channels
+    // beyond the row, a gate) leave the compiler no count of them, so that it waits for all before the first sum; it was
+    // 237 us without and 221 so all the same.  The last row is asked for twice.
     constexpr bool AHEAD = VEC && EL == 4;
     typename BnMap<EL, VEC>::template Raw<T> ry, rz, rh;
     typename BnMap<EL, VEC>::template Raw<R> rx, rr;

@@ -37,7 +37,7 @@
 // waves left in LDS.  With more heads and sequences than CUs a chunk of 128 x 128 takes a
 // wave of two tiles 12000 cycles, 5800 of them matrix instructions.  prep is bound by its solves in float32 and
 // their LDS reads (110 us for 8192 chunk-heads of 128, of 55 us of bytes), chunk by waiting for 256 KB a head,
-// which nothing overlaps (885 us for 8192 of 128 x 128, 470 at the copy's rate).
+// which nothing overlaps, with 54 registers spilled (915 us for 8192 of 128 x 128, 470 at the copy's rate).
 #pragma once
 
 #include "la_walk.h"
@@ -368,7 +368,8 @@ inline dim3 gd_grid(const GdArgs& a, int nblk) {
 // Waves of a walk's workgroup and column tiles of each; one wave: a team (gdelta_team.h).  A wave is bound by the
 // instructions that it can issue and its workgroup by the operands that it reads from LDS, so that the fewest waves
 // to a CU are the quickest where there are CUs left, and two tiles to a wave, which share operands, where
-// there are none.  Microseconds of a forward of 2048 tokens (teams, two waves, four, four of two tiles):
+// there are none.  Sequences count alike whatever their lengths (a long one among many short ones is not walked
+// as quickly as it could be).  Microseconds of a forward of rows of 2048 tokens (teams, two waves, four, four of two tiles):
 //   bf16, 128 x 128  256 tiles 85 116 - 195, 320 146 120 - 197, 512 166 130 135 207, 768 240 243 160 227,
 //                    1024 321 267 190 250; of 1024 tokens 1536 248 199 161 145, 2048 332 272 190 176
 //   float32          256 152 344 - 585, 512 284 390 385 635, 768 438 758 432 681, 1024 581 798 468 719;

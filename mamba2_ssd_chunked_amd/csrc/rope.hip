@@ -8,7 +8,8 @@
 
 namespace ssd {
 
-// V: neighbouring channels that a thread moves at once, 8, or 1 where sizes or alignment ask for it.
+// V: neighbouring channels that a thread moves at once, 8, or 1 where sizes or alignment ask for it (16384 tokens of 40
+// heads of 96 in bf16, 24 channels turned: 39 us in neighbouring pairs, 112 in halves, which go one by one).
 template <typename T, int V>
 __global__ void __launch_bounds__(256) k_rope(RopeArgs a) {
     // rows are known to be aligned to 16 bytes, or to their elements, and no further
