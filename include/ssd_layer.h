@@ -70,7 +70,8 @@ size_t ssd_gdelta_workspace_bytes(const ssd_gdelta* problem, int32_t nseq, int32
  *   o          [batch][seqlen][H][valdim]; tokens outside every sequence are
  *              left as they were                                              (out)
  *   final_state [nseq][H][valdim][keydim] float32 or NULL: the state after each
- *              sequence's last token (its init where it is empty)             (out) */
+ *              sequence's last token (its init where it is empty); may be init itself (out)
+ * No other output may share memory with an input. */
 int ssd_gdelta_fwd(const ssd_gdelta* problem, int32_t nseq, const void* q, const void* k,
                    const void* v, const float* g, const float* beta, const int32_t* cu_seqlens,
                    const float* init, void* o, float* final_state, void* ws, size_t ws_bytes,
