@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(DK * 4) k_gd_chunk(GdArgs a, LaPlan plan) {
         const int64_t row0 = (int64_t)h * a.tokens + t0;
         if (m > 0) __syncthreads();  // the last head's reads are done
         // All that a head reads is asked for at once, but for G: one wait where each piece would have its own
-        // (8192 chunks of 128 x 128: 930 us, 885 so; 23 chunks of 64 x 64: 49, 41).
+        // (8192 chunks of 128 x 128: 930 us, 885 so, 915 with rates as given; 23 chunks of 64 x 64: 49, 41).
         typedef T t4 __attribute__((ext_vector_type(4)));
         constexpr int VPR = DV / 8, NX = GD_Q * VPR / NTHR;  // runs of eight value channels of a row, of a thread
         static_assert(GD_Q * VPR % NTHR == 0, "the threads tile the rows");
